@@ -13,24 +13,18 @@
 #include <vector>
 
 #include "molora.h"
+#include "capi_internal.h"
 #include "molora_launch.h"
 
 static_assert(MOLORA_NOALLOC_SCRATCH_BYTES == molora::kScratchBytes, "scratch size in the header and the library");
 
-struct molora_hotset {
-  int K = 0, r = 0, r_pad = 0, layout = 0, n_targets = 0;
-  float scale = 1.f;
-  bool transposed = false;  // holds (B^T, A^T) of the given adapters (molora_hotset_init_transposed)
-  std::vector<molora::TargetDev> tg;
-  void* slab = nullptr;
-  size_t slab_bytes = 0;
-  // host copies of every adapter's slot addresses, [target][adapter] (both layouts)
-  std::vector<std::vector<uint16_t*>> slotA, slotB;
-};
-
 namespace {
 
 thread_local std::string g_err;
+
+}  // namespace
+
+namespace molora {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -51,7 +45,14 @@ int hip_fail(hipError_t e, const char* what) {
   return fail(MOLORA_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace molora
+
+using molora::aligned;
+using molora::fail;
+using molora::hip_fail;
+using molora::ok;
+
+namespace {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -862,30 +863,21 @@ int molora_router_backward(const void* x, int N, int d, const void* W1, const fl
   return e == hipSuccess ? ok() : hip_fail(e, "router_backward launch");
 }
 
-namespace {
+}  // extern "C"
 
-// Shapes of the decoder's seven LoRA targets (q, k, v, o, gate, up, down).
+namespace molora {
+
 void xf_dims(int d, int f, int* din, int* dout) {
-  const int di[molora::kXfTargets] = {d, d, d, d, d, d, f};
-  const int dn[molora::kXfTargets] = {d, d, d, d, f, f, d};
-  for (int t = 0; t < molora::kXfTargets; ++t) {
+  const int di[kXfTargets] = {d, d, d, d, d, d, f};
+  const int dn[kXfTargets] = {d, d, d, d, f, f, d};
+  for (int t = 0; t < kXfTargets; ++t) {
     din[t] = di[t];
     dout[t] = dn[t];
   }
 }
 
-// Validates the model description; on success *K is the adapters per target (0: no layer
-// has LoRA) and *lora_bytes the largest workspace of one layer's applies.
-int xf_check(int d, int f, int n_layers, const molora_xf_layer* layers, int n_seq, int seq_len, int k, int* K,
-             size_t* lora_bytes, int* paths) {
-  if (d <= 0 || f <= 0 || d % 128 != 0 || f % 128 != 0)
-    return fail(MOLORA_ENOTSUP, "d=%d and f=%d must be positive multiples of 128", d, f);
-  if (n_layers < 1 || n_layers > 1024 || layers == nullptr) return fail(MOLORA_EINVAL, "n_layers=%d or layers", n_layers);
-  if (n_seq < 1 || seq_len < 1) return fail(MOLORA_EINVAL, "n_seq=%d seq_len=%d", n_seq, seq_len);
-  const long long N = (long long)n_seq * seq_len;
-  if (N * std::max(d, f) >= (1ll << 31) || (long long)n_seq * (d / 128) * seq_len * (long long)seq_len >= (1ll << 31))
-    return fail(MOLORA_ENOTSUP, "batch too large");
-  if (k < 1 || k > MOLORA_MAX_TOPK) return fail(MOLORA_ENOTSUP, "k=%d outside [1, %d]", k, MOLORA_MAX_TOPK);
+int xf_check_layers(int d, int f, int n_layers, const molora_xf_layer* layers, long long N, int k, int* K,
+                    size_t* lora_bytes, int* paths) {
   int din[molora::kXfTargets], dout[molora::kXfTargets];
   xf_dims(d, f, din, dout);
   *K = 0;
@@ -925,6 +917,43 @@ int xf_check(int d, int f, int n_layers, const molora_xf_layer* layers, int n_se
   return MOLORA_OK;
 }
 
+void xf_layers_dev(int n_layers, const molora_xf_layer* layers, XfLayerDev* dev) {
+  for (int l = 0; l < n_layers; ++l) {
+    const molora_xf_layer& L = layers[l];
+    XfLayerDev& D = dev[l];
+    D.norm1 = static_cast<const uint16_t*>(L.norm1);
+    D.norm2 = static_cast<const uint16_t*>(L.norm2);
+    for (int t = 0; t < kXfTargets; ++t) D.W[t] = static_cast<const uint16_t*>(L.W[t]);
+    D.lora = L.lora != nullptr;
+    if (D.lora) {
+      for (int t = 0; t < kXfTargets; ++t) D.tgt[t] = L.lora->tg[t];
+      D.indirect = L.lora->layout == MOLORA_LAYOUT_INDIRECT;
+      D.scale = L.lora->scale;
+    }
+  }
+}
+
+}  // namespace molora
+
+extern "C" {
+
+namespace {
+
+// Validates the model description; on success *K is the adapters per target (0: no layer
+// has LoRA) and *lora_bytes the largest workspace of one layer's applies.
+int xf_check(int d, int f, int n_layers, const molora_xf_layer* layers, int n_seq, int seq_len, int k, int* K,
+             size_t* lora_bytes, int* paths) {
+  if (d <= 0 || f <= 0 || d % 128 != 0 || f % 128 != 0)
+    return fail(MOLORA_ENOTSUP, "d=%d and f=%d must be positive multiples of 128", d, f);
+  if (n_layers < 1 || n_layers > 1024 || layers == nullptr) return fail(MOLORA_EINVAL, "n_layers=%d or layers", n_layers);
+  if (n_seq < 1 || seq_len < 1) return fail(MOLORA_EINVAL, "n_seq=%d seq_len=%d", n_seq, seq_len);
+  const long long N = (long long)n_seq * seq_len;
+  if (N * std::max(d, f) >= (1ll << 31) || (long long)n_seq * (d / 128) * seq_len * (long long)seq_len >= (1ll << 31))
+    return fail(MOLORA_ENOTSUP, "batch too large");
+  if (k < 1 || k > MOLORA_MAX_TOPK) return fail(MOLORA_ENOTSUP, "k=%d outside [1, %d]", k, MOLORA_MAX_TOPK);
+  return molora::xf_check_layers(d, f, n_layers, layers, N, k, K, lora_bytes, paths);
+}
+
 }  // namespace
 
 int molora_xf_workspace(int d, int f, int n_layers, const molora_xf_layer* layers, int n_seq, int seq_len, int k,
@@ -958,19 +987,7 @@ int molora_xf_forward(int d, int f, int n_layers, const molora_xf_layer* layers,
   if (ws == nullptr || ws_bytes < plan.total || !aligned(ws, 256))
     return fail(MOLORA_ENOSPC, "workspace of %zu bytes (256-byte aligned) needed, %zu given", plan.total, ws_bytes);
   std::vector<molora::XfLayerDev> dev(n_layers);
-  for (int l = 0; l < n_layers; ++l) {
-    const molora_xf_layer& L = layers[l];
-    molora::XfLayerDev& D = dev[l];
-    D.norm1 = static_cast<const uint16_t*>(L.norm1);
-    D.norm2 = static_cast<const uint16_t*>(L.norm2);
-    for (int t = 0; t < molora::kXfTargets; ++t) D.W[t] = static_cast<const uint16_t*>(L.W[t]);
-    D.lora = L.lora != nullptr;
-    if (D.lora) {
-      for (int t = 0; t < molora::kXfTargets; ++t) D.tgt[t] = L.lora->tg[t];
-      D.indirect = L.lora->layout == MOLORA_LAYOUT_INDIRECT;
-      D.scale = L.lora->scale;
-    }
-  }
+  molora::xf_layers_dev(n_layers, layers, dev.data());
   const char* what = "";
   molora::XfLaunch a{};
   a.d = d; a.f = f; a.n_seq = n_seq; a.seq_len = seq_len; a.n_layers = n_layers; a.K = K; a.k = k;
