@@ -16,3 +16,8 @@ from .binding import (  # noqa: F401
     molora_route_topk_backward, molora_router_backward, molora_router_backward_workspace,
     XfModel, XF_TARGETS, molora_xf_workspace, molora_xf_forward,
 )
+from .decoder import (  # noqa: F401
+    E4M3, SCORE_SIGMOID, SCORE_SOFTMAX, KvCache, decoder_symbols,
+    molora_attn_backward, molora_attn_backward_workspace, molora_attn_decode, molora_attn_decode_workspace,
+    molora_attn_forward, molora_kv_append, molora_route_scores, molora_route_scores_backward,
+)

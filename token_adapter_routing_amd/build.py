@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmolora.so")
-SOURCES = ["capi.cpp", "plan.cpp", "route.hip", "dispatch.hip", "apply.hip", "dense.hip", "gsplit.hip", "backward.hip", "xf.hip", "xfmr.cpp"]
+SOURCES = ["capi.cpp", "plan.cpp", "route.hip", "dispatch.hip", "apply.hip", "dense.hip", "gsplit.hip", "backward.hip", "xf.hip", "xfmr.cpp",
+           "capi_decoder.cpp", "decoder_plan.cpp", "route_scores.hip", "attn.hip", "kvcache.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

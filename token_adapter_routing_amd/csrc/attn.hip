@@ -1,0 +1,519 @@
+// Causal attention over packed sequences with a window and sink tokens, forward and backward.
+//
+//   forward   S = scale Q K^T over the visible pairs, O = softmax(S) V, lse = log sum exp S
+//   backward  P = exp(S - lse), dV = P^T dO, dP = dO V^T, dS = P (dP - rowsum(dO O)),
+//             dQ = scale dS K, dK = scale dS^T Q
+//
+// One pass over the keys per query tile with the running maximum and sum of the softmax; S, P and
+// dS exist only in registers.  Products run on 32x32x16 bf16 matrix instructions, arranged so
+// that a product's result is the next one's operand as it stands: the forward computes S^T (keys
+// down, queries across), so a lane holds 16 keys of one query, the softmax's maximum and sum are
+// sums over registers and one exchange between the wave's halves, and P^T, rounded to bf16, is
+// the right operand of O^T = V^T P^T.  The operand that has to be read along its columns (V, and
+// in the backward K, Q, dO) comes from LDS through the transposing 8-byte read.
+//
+// Tiles lie in LDS as rows of D values whose 16-byte pieces are permuted by the row (Tile::off),
+// so that both the row reads (32 rows, one piece each) and the transposing reads (4 rows, four
+// neighbouring pieces each) touch every bank once.
+#include <cmath>
+
+#include "decoder_launch.h"
+#include "seq_dev.h"
+
+namespace molora {
+
+namespace {
+
+constexpr int kBN = 64;  // keys per LDS tile of the forward and the dq pass
+constexpr int kBQ = 32;  // queries per LDS tile of the dk / dv pass
+
+template <int D>
+struct Tile {
+  static constexpr int kRow = 2 * D;        // bytes
+  static constexpr int kPieces = D / 8;     // 16-byte pieces per row
+  static __device__ __forceinline__ int swz(int row) {
+    if constexpr (D == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+    else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  }
+  static __device__ __forceinline__ int off(int row, int piece) { return row * kRow + ((piece ^ swz(row)) << 4); }
+};
+
+// Copies ROWS rows of a packed tensor into an LDS tile by way of registers: load() requests, store()
+// writes.  Rows past `last` repeat row `last`.
+template <int D, int ROWS>
+struct Stage {
+  static constexpr int kN = ROWS * Tile<D>::kPieces / 256;
+  u32x4_t r[kN];
+  __device__ __forceinline__ void load(const uint16_t* base, uint32_t stride, int row0, int last, int tid) {
+    const uint16_t* p = base + (long long)row0 * stride;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int id = tid + 256 * i, row = id / Tile<D>::kPieces, c = id % Tile<D>::kPieces;
+      r[i] = ld16(p + (uint32_t)(min(row, last - row0) * stride + c * 8));
+    }
+  }
+  __device__ __forceinline__ void store(char* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int id = tid + 256 * i, row = id / Tile<D>::kPieces, c = id % Tile<D>::kPieces;
+      st16(lds + Tile<D>::off(row, c), r[i]);
+    }
+  }
+};
+
+// Left operand (rows down): row `row` of the tile, values 16 st + 8 h .. + 7.
+template <int D>
+__device__ __forceinline__ bf16x8_t row_frag(const char* lds, int row, int st, int h) {
+  return as_bf16x8(ld16(lds + Tile<D>::off(row, 2 * st + h)));
+}
+
+// Left operand (columns down): column 32 mb + lane % 32 of the tile; k-slots 0..3 are rows
+// row0 + 4 h + 0..3, k-slots 4..7 rows row0 + 8 + 4 h + 0..3, the order in which a 32x32 result
+// holds its rows.  Each group of 16 lanes reads a 4 x 16 block and gets its columns.
+template <int D>
+__device__ __forceinline__ bf16x8_t col_frag(const char* lds, int row0, int mb, int lane) {
+  typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+  const int h = lane >> 5, q = lane & 15, col = 32 * mb + (lane & 16) + 4 * (q & 3), row = row0 + 4 * h + (q >> 2);
+  const char* a = lds + Tile<D>::off(row, col >> 3) + (col & 4) * 2;
+  const char* b = lds + Tile<D>::off(row + 8, col >> 3) + (col & 4) * 2;
+  union {
+    s16x4_t s[2];
+    bf16x8_t v;
+  } u;
+  u.s[0] = __builtin_bit_cast(s16x4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a));
+  u.s[1] = __builtin_bit_cast(s16x4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b));
+  return u.v;
+}
+
+// Right operand from registers: rows 16 s .. + 15 of a 32x32 result, rounded to bf16.
+__device__ __forceinline__ bf16x8_t acc_frag(const f32x16_t& v, int s) {
+  u32x4_t u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(v[8 * s + 2 * i], v[8 * s + 2 * i + 1]);
+  return as_bf16x8(u);
+}
+
+__device__ __forceinline__ int acc_row(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
+
+// A query tile: sequence, first row, lengths, first rows in the packed tensors.
+struct QTile {
+  int row0, Lq, Lk, q0, k0;
+  bool ok;
+};
+__device__ __forceinline__ QTile find_q_tile(const AttnArgs& a, long long slot) {
+  QTile t{};
+  const int s = __builtin_amdgcn_readfirstlane(
+      wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.q_off[i], 0), a.Tq), i, kAttnQ); }));
+  if (s < 0) return t;
+  const SeqRange q = seq_range(a.q_off, s, a.Tq), k = seq_range(a.kv_off, s, a.Tkv);
+  const long long row0 = (slot - attn_slot0(q.lo, s, kAttnQ)) * kAttnQ;
+  t.row0 = (int)row0;
+  t.Lq = q.n;
+  t.Lk = k.n;
+  t.q0 = q.lo;
+  t.k0 = k.lo;
+  t.ok = row0 >= 0 && row0 < q.n;
+  return t;
+}
+
+// Key tiles a query tile visits: the sinks' first, then the window's.
+struct KeyTiles {
+  int sink, lo, n;
+  __device__ __forceinline__ int at(int i) const { return (i < sink ? i : lo + i - sink) * kBN; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const Mask& m, int p_lo, int p_hi, int Lk) {
+  KeyTiles t;
+  const int hi = min(p_hi + 1, Lk);  // keys below hi may be seen
+  const int first = m.window ? max(p_lo - m.window + 1, 0) : 0;
+  t.lo = first / kBN;
+  t.sink = m.window ? min((min(m.sinks, max(hi, 0)) + kBN - 1) / kBN, t.lo) : 0;
+  t.n = t.sink + max((hi + kBN - 1) / kBN - t.lo, 0);
+  if (hi <= 0) t.n = 0;
+  return t;
+}
+
+// Whether rows at positions [p_lo, p_hi] see nothing, or everything, of keys [j0, j1].
+__device__ __forceinline__ bool sees_none(const Mask& m, int p_lo, int p_hi, int j0, int j1) {
+  return j0 > p_hi || (m.window && j1 <= p_lo - m.window && j0 >= m.sinks);
+}
+__device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int j0, int j1) {
+  return j1 <= p_lo && (!m.window || j0 > p_hi - m.window || j1 < m.sinks);
+}
+
+// Workgroup -> (head, slot): the heads of one key-value head follow each other on one XCD
+// (consecutive workgroups go round the XCDs), the longest tiles of a sequence come first.
+struct Place {
+  int hq, hk;
+  long long slot;
+};
+__device__ __forceinline__ Place place(const AttnArgs& a, long long slots) {
+  const int g = a.Hq / a.Hkv;
+  const long long id = blockIdx.x;
+  const int hk = (int)(id % a.Hkv);
+  const long long rest = id / a.Hkv;
+  return {hk * g + (int)(rest % g), hk, slots - 1 - rest / g};
+}
+
+// Stores a 32 x D block held as D x 32 (column = row of the output), times `mul`.
+template <int D>
+__device__ __forceinline__ void store_rows(uint16_t* row, const f32x16_t* acc, float mul, int h) {
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint2 v;
+      v.x = pack_bf16x2(acc[mb][4 * g] * mul, acc[mb][4 * g + 1] * mul);
+      v.y = pack_bf16x2(acc[mb][4 * g + 2] * mul, acc[mb][4 * g + 3] * mul);
+      *reinterpret_cast<uint2*>(row + 32 * mb + 8 * g + 4 * h) = v;
+    }
+}
+
+}  // namespace
+
+// A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kTileB = kBN * Tile<D>::kRow;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
+            n = lane & 31;
+  const Place pl = place(a, slots);
+  const QTile t = find_q_tile(a, pl.slot);
+  if (!t.ok) return;
+  const Mask m{t.Lk - t.Lq, a.window, a.sinks};
+  const int last = t.Lq - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.Lk);
+  const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
+  const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
+  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + pl.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + pl.hk * a.v.head;
+  bf16x8_t q[D / 16];
+  {
+    const uint16_t* qr = a.q.p + (long long)(t.q0 + r) * a.q.token + pl.hq * a.q.head + 8 * h;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) q[st] = as_bf16x8(ld16(qr + 16 * st));
+  }
+  f32x16_t o[D / 32];
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb) o[mb] = f32x16_t{};
+  const float c = a.scale * kLog2e;  // the softmax in base 2
+  float mx = -INFINITY, sum = 0.f;   // reference maximum of c s; the lane's part of the sum
+  Stage<D, kBN> sk, sv;
+  if (kt.n > 0) {
+    sk.load(kb, (uint32_t)a.k.token, kt.at(0), t.Lk - 1, tid);
+    sv.load(vb, (uint32_t)a.v.token, kt.at(0), t.Lk - 1, tid);
+    sk.store(lds, tid);
+    sv.store(lds + 2 * kTileB, tid);
+  }
+  __syncthreads();
+  for (int it = 0; it < kt.n; ++it) {
+    const int j0 = kt.at(it);
+    const char* K = lds + (it & 1) * kTileB;
+    const char* V = lds + (2 + (it & 1)) * kTileB;
+    const bool more = it + 1 < kt.n;
+    if (more) {
+      sk.load(kb, (uint32_t)a.k.token, kt.at(it + 1), t.Lk - 1, tid);
+      sv.load(vb, (uint32_t)a.v.token, kt.at(it + 1), t.Lk - 1, tid);
+    }
+    if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
+      f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s[b] = mfma32x32x16(row_frag<D>(K, 32 * b + n, st, h), q[st], s[b]);
+      if (!sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[b][i] = m.sees(p, j0 + 32 * b + acc_row(i, h)) ? s[b][i] : -INFINITY;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+      top *= c;
+      // The reference follows the maximum only when it is left behind by more than 2^8: until then the
+      // weights stay below 2^8, which costs no precision in floating point.
+      if (__any(top > mx + 8.f)) {
+        const float up = fmaxf(mx, fmaxf(top, __shfl_xor(top, 32, kWave)));
+        const float f = up > -INFINITY ? exp2_hw(mx - up) : 1.f;
+        mx = up;
+        sum *= f;
+#pragma unroll
+        for (int mb = 0; mb < D / 32; ++mb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[mb][i] *= f;
+      }
+      const float ref = mx > -INFINITY ? mx : 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[b][i] = exp2_hw(fmaf(s[b][i], c, -ref));
+          sum += s[b][i];
+        }
+#pragma unroll
+      for (int st = 0; st < kBN / 16; ++st) {
+        const bf16x8_t pf = acc_frag(s[st >> 1], st & 1);
+#pragma unroll
+        for (int mb = 0; mb < D / 32; ++mb) o[mb] = mfma32x32x16(col_frag<D>(V, 16 * st, mb, lane), pf, o[mb]);
+      }
+    }
+    if (more) {
+      sk.store(lds + ((it + 1) & 1) * kTileB, tid);
+      sv.store(lds + (2 + ((it + 1) & 1)) * kTileB, tid);
+    }
+    __syncthreads();
+  }
+  sum += __shfl_xor(sum, 32, kWave);
+  if (r0 + n > last) return;
+  store_rows<D>(a.o.p + (long long)(t.q0 + r) * a.o.token + pl.hq * a.o.head, o, sum > 0.f ? 1.f / sum : sum, h);
+  if (a.lse != nullptr && h == 0)
+    a.lse[(size_t)pl.hq * a.Tq + t.q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+}
+
+// dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
+// the keys as the forward does.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long long slots) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kTileB = kBN * Tile<D>::kRow;
+  const AttnArgs& a = b.f;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
+            n = lane & 31;
+  const Place pl = place(a, slots);
+  const QTile t = find_q_tile(a, pl.slot);
+  if (!t.ok) return;
+  const Mask m{t.Lk - t.Lq, a.window, a.sinks};
+  const int last = t.Lq - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.Lk);
+  const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
+  const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
+  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + pl.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + pl.hk * a.v.head;
+  bf16x8_t q[D / 16], g[D / 16];
+  float delta = 0.f;
+  {
+    const long long row = t.q0 + r;
+    const uint16_t* qr = a.q.p + row * a.q.token + pl.hq * a.q.head + 8 * h;
+    const uint16_t* gr = b.dout.p + row * b.dout.token + pl.hq * b.dout.head + 8 * h;
+    const uint16_t* orow = a.o.p + row * a.o.token + pl.hq * a.o.head + 8 * h;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      q[st] = as_bf16x8(ld16(qr + 16 * st));
+      const u32x4_t gv = ld16(gr + 16 * st), ov = ld16(orow + 16 * st);
+      g[st] = as_bf16x8(gv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        delta = fmaf(bf16_to_f32(gv[i] & 0xffffu), bf16_to_f32(ov[i] & 0xffffu), delta);
+        delta = fmaf(bf16_to_f32(gv[i] >> 16), bf16_to_f32(ov[i] >> 16), delta);
+      }
+    }
+    delta += __shfl_xor(delta, 32, kWave);
+  }
+  const size_t stat = (size_t)pl.hq * a.Tq + t.q0 + r;
+  const float lse2 = a.lse[stat] * kLog2e;
+  if (h == 0 && r0 + n <= last) b.delta[stat] = delta;
+  f32x16_t dq[D / 32];
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb) dq[mb] = f32x16_t{};
+  const float c = a.scale * kLog2e;
+  Stage<D, kBN> sk, sv;
+  if (kt.n > 0) {
+    sk.load(kb, (uint32_t)a.k.token, kt.at(0), t.Lk - 1, tid);
+    sv.load(vb, (uint32_t)a.v.token, kt.at(0), t.Lk - 1, tid);
+    sk.store(lds, tid);
+    sv.store(lds + 2 * kTileB, tid);
+  }
+  __syncthreads();
+  for (int it = 0; it < kt.n; ++it) {
+    const int j0 = kt.at(it);
+    const char* K = lds + (it & 1) * kTileB;
+    const char* V = lds + (2 + (it & 1)) * kTileB;
+    const bool more = it + 1 < kt.n;
+    if (more) {
+      sk.load(kb, (uint32_t)a.k.token, kt.at(it + 1), t.Lk - 1, tid);
+      sv.load(vb, (uint32_t)a.v.token, kt.at(it + 1), t.Lk - 1, tid);
+    }
+    if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
+      const bool all = sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1);
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {
+          s = mfma32x32x16(row_frag<D>(K, 32 * blk + n, st, h), q[st], s);
+          dp = mfma32x32x16(row_frag<D>(V, 32 * blk + n, st, h), g[st], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = exp2_hw(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+          s[i] = all || m.sees(p, j0 + 32 * blk + acc_row(i, h)) ? e : 0.f;
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const bf16x8_t df = acc_frag(s, st);
+#pragma unroll
+          for (int mb = 0; mb < D / 32; ++mb)
+            dq[mb] = mfma32x32x16(col_frag<D>(K, 32 * blk + 16 * st, mb, lane), df, dq[mb]);
+        }
+      }
+    }
+    if (more) {
+      sk.store(lds + ((it + 1) & 1) * kTileB, tid);
+      sv.store(lds + (2 + ((it + 1) & 1)) * kTileB, tid);
+    }
+    __syncthreads();
+  }
+  if (r0 + n <= last)
+    store_rows<D>(b.dq.p + (long long)(t.q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
+}
+
+// dK and dV: a workgroup holds 128 keys of one key-value head, 32 per wave, and walks the queries
+// of every query head that reads it.  S and dP are computed with the queries down, so that P and
+// dS are the right operands of dV^T = dO^T P and dK^T = Q^T dS.
+template <int D>
+__global__ __launch_bounds__(256, 1) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kTileB = kBQ * Tile<D>::kRow;
+  const AttnArgs& a = b.f;
+  float* stats = reinterpret_cast<float*>(lds + 4 * kTileB);  // [2][2][kBQ]: lse in base 2, row sums
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
+            n = lane & 31;
+  const int group = a.Hq / a.Hkv;
+  const int hk = (int)(blockIdx.x % a.Hkv);
+  const long long slot = blockIdx.x / a.Hkv;  // the first keys are seen by the most queries
+  const int sq = __builtin_amdgcn_readfirstlane(
+      wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.kv_off[i], 0), a.Tkv), i, kAttnK); }));
+  if (sq < 0) return;
+  const SeqRange qr = seq_range(a.q_off, sq, a.Tq), kr = seq_range(a.kv_off, sq, a.Tkv);
+  const long long kt0 = (slot - attn_slot0(kr.lo, sq, kAttnK)) * kAttnK;
+  if (kt0 < 0 || kt0 >= kr.n) return;
+  const int k0 = (int)kt0, Lq = qr.n, Lk = kr.n;
+  const Mask m{Lk - Lq, a.window, a.sinks};
+  const int jw = k0 + 32 * wave, j = jw + n, jr = min(j, Lk - 1);  // wave's first key, lane's key
+  bf16x8_t kf[D / 16], vf[D / 16];
+  {
+    const uint16_t* kp = a.k.p + (long long)(kr.lo + jr) * a.k.token + hk * a.k.head + 8 * h;
+    const uint16_t* vp = a.v.p + (long long)(kr.lo + jr) * a.v.token + hk * a.v.head + 8 * h;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      kf[st] = as_bf16x8(ld16(kp + 16 * st));
+      vf[st] = as_bf16x8(ld16(vp + 16 * st));
+    }
+  }
+  // queries that see any of the workgroup's keys: [i_lo, i_hi)
+  const int i_lo = max(k0 - m.shift, 0);
+  int i_hi = Lq;
+  if (m.window && k0 >= m.sinks) {
+    const long long end = (long long)min(k0 + kAttnK, Lk) - 1 + m.window - m.shift;
+    i_hi = (int)max(0ll, min((long long)Lq, end));
+  }
+  const int t_lo = i_lo / kBQ, nt = max((i_hi + kBQ - 1) / kBQ - t_lo, 0), total = nt * group;
+  f32x16_t dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb) dk[mb] = dv[mb] = f32x16_t{};
+  const float c = a.scale * kLog2e;
+  Stage<D, kBQ> s_q, s_g;
+  float st_v = 0.f;
+  auto load = [&](int it) {
+    const int hq = hk * group + it / nt, i0 = (t_lo + it % nt) * kBQ;
+    s_q.load(a.q.p + (long long)qr.lo * a.q.token + hq * a.q.head, (uint32_t)a.q.token, i0, Lq - 1, tid);
+    s_g.load(b.dout.p + (long long)qr.lo * b.dout.token + hq * b.dout.head, (uint32_t)b.dout.token, i0, Lq - 1, tid);
+    if (tid < 2 * kBQ) {
+      const size_t at = (size_t)hq * a.Tq + qr.lo + min(i0 + (tid & (kBQ - 1)), Lq - 1);
+      st_v = tid < kBQ ? a.lse[at] * kLog2e : b.delta[at];
+    }
+  };
+  auto store = [&](int buf) {
+    s_q.store(lds + buf * kTileB, tid);
+    s_g.store(lds + (2 + buf) * kTileB, tid);
+    if (tid < 2 * kBQ) stats[buf * 2 * kBQ + tid] = st_v;
+  };
+  if (total > 0) {
+    load(0);
+    store(0);
+  }
+  __syncthreads();
+  for (int it = 0; it < total; ++it) {
+    const int i0 = (t_lo + it % nt) * kBQ, buf = it & 1;
+    const char* Q = lds + buf * kTileB;
+    const char* G = lds + (2 + buf) * kTileB;
+    const float* ls = stats + buf * 2 * kBQ;
+    const bool more = it + 1 < total;
+    if (more) load(it + 1);
+    const int p_lo = i0 + m.shift, p_hi = min(i0 + kBQ - 1, Lq - 1) + m.shift;
+    if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
+      const bool all = i0 + kBQ <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
+      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) {
+        s = mfma32x32x16(row_frag<D>(Q, n, st, h), kf[st], s);
+        dp = mfma32x32x16(row_frag<D>(G, n, st, h), vf[st], dp);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + 8 * g + 4 * h);
+        const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + 8 * g + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i0 + 8 * g + 4 * h + i;
+          const bool on = all || (row < Lq && m.sees(row + m.shift, j));
+          const float pv = on ? exp2_hw(fmaf(s[4 * g + i], c, -l4[i])) : 0.f;
+          s[4 * g + i] = pv;
+          dp[4 * g + i] = on ? pv * (dp[4 * g + i] - d4[i]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const bf16x8_t pf = acc_frag(s, st), df = acc_frag(dp, st);
+#pragma unroll
+        for (int mb = 0; mb < D / 32; ++mb) {
+          dv[mb] = mfma32x32x16(col_frag<D>(G, 16 * st, mb, lane), pf, dv[mb]);
+          dk[mb] = mfma32x32x16(col_frag<D>(Q, 16 * st, mb, lane), df, dk[mb]);
+        }
+      }
+    }
+    if (more) store(buf ^ 1);
+    __syncthreads();
+  }
+  if (j >= Lk) return;
+  store_rows<D>(b.dk.p + (long long)(kr.lo + j) * b.dk.token + hk * b.dk.head, dk, a.scale, h);
+  store_rows<D>(b.dv.p + (long long)(kr.lo + j) * b.dv.token + hk * b.dv.head, dv, 1.f, h);
+}
+
+namespace {
+
+template <int D>
+hipError_t forward(const AttnArgs& a, hipStream_t s) {
+  const long long slots = attn_slots(a.Tq, a.n_seq, kAttnQ);
+  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 4 * kBN * Tile<D>::kRow, s, a, slots);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
+  const AttnArgs& a = b.f;
+  const long long qs = attn_slots(a.Tq, a.n_seq, kAttnQ), ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
+  if (a.Tq > 0) {
+    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 4 * kBN * Tile<D>::kRow, s, b, qs);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)(ks * a.Hkv)), dim3(256),
+                     4 * kBQ * Tile<D>::kRow + 4 * kBQ * sizeof(float), s, b, ks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t s) {
+  return a.D == 64 ? forward<64>(a, s) : forward<128>(a, s);
+}
+
+hipError_t launch_attn_backward(const AttnBackwardArgs& b, hipStream_t s) {
+  return b.f.D == 64 ? backward<64>(b, s) : backward<128>(b, s);
+}
+
+}  // namespace molora

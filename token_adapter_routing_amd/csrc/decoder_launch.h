@@ -1,0 +1,81 @@
+// Host-side launchers of the decoder's operators (internal to the library).  Every launcher
+// assumes its arguments were validated by the C-ABI layer and only enqueues work.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "decoder_plan.h"
+
+namespace molora {
+
+enum { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+
+struct RouteScoresArgs {
+  const float* logits;
+  const float* bias;  // or NULL
+  int N, K, k, score, n_group, topk_group, renorm;
+  float factor;
+  int32_t* idx;  // the backward reads it
+  float* w;
+};
+hipError_t launch_route_scores(const RouteScoresArgs& a, hipStream_t s);
+hipError_t launch_route_scores_backward(const RouteScoresArgs& a, const float* dw, float* dl, hipStream_t s);
+
+// Rows of packed tensors: element strides between tokens and heads.
+struct Rows {
+  uint16_t* p;
+  long long token, head;
+};
+struct AttnArgs {
+  Rows q, k, v, o;
+  float* lse;  // [Hq][Tq] or NULL
+  const int32_t* q_off;
+  const int32_t* kv_off;
+  int n_seq, Hq, Hkv, D, Tq, Tkv, window, sinks;
+  float scale;
+};
+hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t s);
+
+struct AttnBackwardArgs {
+  AttnArgs f;  // o and lse as the forward wrote them
+  Rows dout, dq, dk, dv;
+  float* delta;  // workspace [Hq][Tq]
+};
+hipError_t launch_attn_backward(const AttnBackwardArgs& a, hipStream_t s);
+
+struct KvCacheDev {
+  void* k;
+  void* v;
+  uint8_t* k_scale;  // e4m3 only
+  uint8_t* v_scale;
+  int n_pages, Hkv, page_shift, D;
+  bool e4m3;
+};
+struct KvAppendArgs {
+  KvCacheDev c;
+  Rows k, v;
+  int T, n_seq;
+  const int32_t* q_off;  // NULL: one row per sequence
+  const int32_t* table;
+  int width;
+  const int32_t* lens;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s);
+
+struct DecodeArgs {
+  KvCacheDev c;
+  Rows q, o;
+  float* lse;  // [n_seq][Hq] or NULL
+  int n_seq, Hq;
+  const int32_t* table;
+  int width;
+  const int32_t* lens;
+  int window, sinks;
+  float scale;
+  int splits;   // decode_plan
+  float* part;  // decode_plan, splits > 1
+};
+hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);
+
+}  // namespace molora

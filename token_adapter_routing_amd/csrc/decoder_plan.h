@@ -1,0 +1,44 @@
+// Sizes and index formulas shared by the host layer and the kernels of the decoder's operators.
+// Plain C++ without HIP types (see molora_plan.h).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "molora_plan.h"
+
+namespace molora {
+
+// ---- attention over packed sequences: query tiles of kAttnQ rows.  Sequence s owns the tile
+// slots from q_off[s] / kAttnQ + s on: floor((a + L) / t) + 1 >= floor(a / t) + ceil(L / t), so
+// the slots of two sequences never meet, a slot's sequence is found by search in q_off itself,
+// and T / kAttnQ + n_seq slots cover every tile.
+constexpr int kAttnQ = 128;   // query rows per workgroup of the forward and the dq pass
+constexpr int kAttnK = 128;   // key rows per workgroup of the dk / dv pass
+MOLORA_HD inline long long attn_slot0(int off, int s, int tile) { return (long long)(off / tile) + s; }
+MOLORA_HD inline long long attn_slots(int T, int n_seq, int tile) { return (long long)(T / tile) + n_seq; }
+
+// backward: rowsum(dO O), fp32 [heads][Tq]
+inline size_t attn_backward_ws_bytes(int Tq, int heads) { return align256((size_t)Tq * heads * sizeof(float)); }
+
+// ---- decode attention: blocks of kDecBlock positions; a sequence's visible blocks are split
+// evenly over `splits` workgroups, at least kDecMinBlocks each.  Partial results per (sequence,
+// head tile, split): kDecHeads rows of head_dim sums (fp32), then the maxima and the sums of
+// weights.
+constexpr int kDecBlock = 32;
+constexpr int kDecHeads = 16;     // query heads per workgroup (one matrix-instruction column block)
+constexpr int kDecMinBlocks = 8;  // two per wave
+struct DecodePlan {
+  int head_tiles;  // workgroups per key-value head: ceil(query heads per kv head / kDecHeads)
+  long long units;  // n_seq * n_kv_heads * head_tiles
+  int splits;
+  size_t part_floats, total;
+};
+DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int page_size, int table_width);
+MOLORA_HD inline size_t decode_part_floats(int head_dim) { return (size_t)kDecHeads * (head_dim + 2); }
+MOLORA_HD inline int decode_blocks_per_split(int blocks, int splits) {
+  const int per = (blocks + splits - 1) / splits;
+  return per < kDecMinBlocks ? kDecMinBlocks : per;
+}
+
+}  // namespace molora

@@ -1,0 +1,326 @@
+// Routing by scores: softmax or sigmoid scores, a balance bias for the selection, adapter
+// groups, top-k, (re)normalised weights; and its gradient.
+//
+//   s = softmax(l) | sigmoid(l);  c = s + bias;  mark_g = sum of group g's two largest c;
+//   keep the topk_group largest marks; choose the k largest c; w = factor s / [renorm] sum s
+//   dl_e = s_e (g_e - sum_j s_j g_j) | s_e (1 - s_e) g_e,
+//   g_j = factor (dw_j - [renorm] sum_i dw_i s_i / S) / [renorm] S over the chosen, S their sum
+//
+// Layout: eight lanes per token, lane i holding adapters [i E, (i + 1) E), E = 2, 4 or 8 with
+// 8 E >= K, so a wave takes eight tokens, a reduction over adapters is E register steps and
+// three exchanges inside eight lanes, and each lane's logits are one contiguous piece.  One
+// round of the selection per chosen adapter (k <= 8).
+#include <cfloat>
+#include <cmath>
+
+#include "decoder_launch.h"
+#include "molora_dev.h"
+
+namespace molora {
+
+namespace {
+
+constexpr int kLanes = 8;             // lanes per token
+constexpr int kTok = kWave / kLanes;  // tokens per wave
+constexpr int kWaves = 4;             // waves per workgroup
+
+template <typename F>
+__device__ __forceinline__ F sum8(F v) {
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
+  return v;
+}
+
+// Lane's E logits of token `tok`; absent adapters (NaN, -inf, past K) come as -inf, +inf as the
+// largest finite number.
+template <int E>
+__device__ __forceinline__ void load_logits(const float* __restrict__ logits, int tok, bool mine, int K, int e0,
+                                            float* l) {
+  const float* row = logits + (size_t)tok * K + e0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) l[j] = -INFINITY;
+  if (mine) {
+    if (K == kLanes * E) {  // whole rows: E a multiple of 2, so 8- or 16-byte pieces
+      if constexpr (E >= 4) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+          const u32x4_t v = ld16(row + 4 * q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[4 * q + j] = __uint_as_float(v[j]);
+        }
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(row);
+        l[0] = v.x;
+        l[1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (e0 + j < K) l[j] = row[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < E; ++j) l[j] = l[j] == l[j] ? fminf(l[j], FLT_MAX) : -INFINITY;
+}
+
+// Scores of the lane's adapters in F; exp(l - top) and 1 / (1 + exp(-l)) as written, so that an
+// absent adapter (-inf) gets exactly 0.
+template <typename F, int E>
+__device__ __forceinline__ void scores(const float* l, int score, F* s) {
+  if (score == kScoreSigmoid) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) s[j] = F(1) / (F(1) + exp(-F(l[j])));
+    return;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < E; ++j) top = fmaxf(top, l[j]);
+  top = max8(top);
+  F total = 0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    s[j] = l[j] > -INFINITY ? exp(F(l[j]) - F(top)) : F(0);
+    total += s[j];
+  }
+  total = sum8(total);
+  const F inv = total > F(0) ? F(1) / total : F(0);
+#pragma unroll
+  for (int j = 0; j < E; ++j) s[j] *= inv;
+}
+
+// Rounds of "largest value, lowest index" over the n values spread over eight lanes (lane i's
+// j-th has index base + j step; values of -inf are never taken).  Returns the taken indices;
+// *gap is the distance between the last one taken and the largest left (inf where none is).
+template <typename F, int E>
+__device__ __forceinline__ uint64_t take_largest(F* v, int base, int step, int rounds, F* gap) {
+  uint64_t taken = 0;
+  F last = INFINITY;
+  *gap = INFINITY;
+  for (int r = 0; r <= rounds; ++r) {
+    F best = -INFINITY;
+    int at = 64;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (v[j] > best) {
+        best = v[j];
+        at = base + j * step;
+      }
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) {
+      const F ov = __shfl_xor(best, d, kWave);
+      const int oa = __shfl_xor(at, d, kWave);
+      if (ov > best || (ov == best && oa < at)) {
+        best = ov;
+        at = oa;
+      }
+    }
+    if (r == rounds) {
+      if (best > -INFINITY) *gap = last - best;
+      break;
+    }
+    last = best;
+    if (best > -INFINITY) {
+      taken |= 1ull << at;
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (base + j * step == at) v[j] = -INFINITY;
+    }
+  }
+  return taken;
+}
+
+// The chosen adapters of the lane's token.  c: the lane's selection values (destroyed).
+// *margin: the narrowest of the decisions' distances.  mem: the wave's kTok * K values.
+template <typename F, int E>
+__device__ __forceinline__ uint64_t choose(F* c, const RouteScoresArgs& a, int t, int lane8, F* mem, F* margin) {
+  *margin = INFINITY;
+  if (a.n_group > 1) {
+    const int gs = a.K / a.n_group;
+    F* row = mem + t * a.K;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (lane8 * E + j < a.K) row[lane8 * E + j] = c[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    F mark[8];  // groups lane8, lane8 + 8, ...
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mark[i] = -INFINITY;
+      const int g = lane8 + kLanes * i;
+      if (g >= a.n_group) continue;
+      F m1 = -INFINITY, m2 = -INFINITY;
+      for (int j = 0; j < gs; ++j) {
+        const F x = row[g * gs + j];
+        if (x > m1) {
+          m2 = m1;
+          m1 = x;
+        } else if (x > m2) {
+          m2 = x;
+        }
+      }
+      mark[i] = m2 > -INFINITY ? m1 + m2 : m1;
+    }
+    const uint64_t kept = take_largest<F, 8>(mark, lane8, kLanes, a.topk_group, margin);
+    const uint32_t inv = (65536u + gs - 1) / gs;  // e / gs for e < 64
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const uint32_t e = lane8 * E + j;
+      if (!((kept >> ((e * inv) >> 16)) & 1ull)) c[j] = -INFINITY;
+    }
+  }
+  F gap;
+  const uint64_t chosen = take_largest<F, E>(c, lane8 * E, 1, a.k, &gap);
+  if (gap < *margin) *margin = gap;
+  return chosen;
+}
+
+}  // namespace
+
+template <int E>
+__global__ __launch_bounds__(kWave * kWaves) void route_scores_k(RouteScoresArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = lane / kLanes, lane8 = lane % kLanes;
+  const int tok = (blockIdx.x * kWaves + wave) * kTok + t;
+  const bool mine = tok < a.N;
+  const int e0 = lane8 * E;
+  float l[E], s[E], b[E];
+  load_logits<E>(a.logits, tok, mine, a.K, e0, l);
+#pragma unroll
+  for (int j = 0; j < E; ++j) b[j] = a.bias != nullptr && e0 + j < a.K ? a.bias[e0 + j] : 0.f;
+  scores<float, E>(l, a.score, s);
+  double* mem = reinterpret_cast<double*>(lds) + (size_t)wave * kTok * a.K;
+  auto can = [&](int j) { return l[j] > -INFINITY && b[j] > -INFINITY; };  // false for a NaN bias
+  uint64_t chosen;
+  if (a.bias == nullptr && a.n_group == 1) {
+    float c[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) c[j] = l[j];
+    float margin;
+    chosen = choose<float, E>(c, a, t, lane8, nullptr, &margin);
+  } else {
+    float c[E], margin, scale = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      c[j] = can(j) ? s[j] + b[j] : -INFINITY;
+      if (can(j)) scale = fmaxf(scale, s[j] + fabsf(b[j]));
+    }
+    chosen = choose<float, E>(c, a, t, lane8, reinterpret_cast<float*>(mem), &margin);
+    // s is within about 8 x 2^-24 of itself, s + bias rounds once and a mark is two of them: decisions
+    // nearer than 2^-19 of the largest magnitude are taken again in 64 bits
+    const float close = max8(scale) * 0x1p-19f;
+    if (__any(mine && !(margin > close))) {
+      double s64[E], gap;
+      scores<double, E>(l, a.score, s64);
+#pragma unroll
+      for (int j = 0; j < E; ++j) s64[j] = can(j) ? s64[j] + (double)b[j] : -INFINITY;
+      chosen = choose<double, E>(s64, a, t, lane8, mem, &gap);
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if ((chosen >> (e0 + j)) & 1ull) sum += s[j];
+  sum = sum8(sum);
+  const float f = a.renorm ? (sum > 0.f ? a.factor / sum : 0.f) : a.factor;
+  if (!mine) return;
+  int32_t* idx = a.idx + (size_t)tok * a.k;
+  float* w = a.w + (size_t)tok * a.k;
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if ((chosen >> (e0 + j)) & 1ull) {
+      const int slot = __popcll(chosen & ((1ull << (e0 + j)) - 1));  // ascending adapter index
+      idx[slot] = e0 + j;
+      w[slot] = s[j] * f;
+    }
+  if (lane8 >= __popcll(chosen) && lane8 < a.k) {
+    idx[lane8] = -1;
+    w[lane8] = 0.f;
+  }
+}
+
+template <int E>
+__global__ __launch_bounds__(kWave * kWaves) void route_scores_bwd_k(RouteScoresArgs a, const float* __restrict__ dw,
+                                                                     float* __restrict__ dl) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = lane / kLanes, lane8 = lane % kLanes;
+  const int tok = (blockIdx.x * kWaves + wave) * kTok + t;
+  const bool mine = tok < a.N;
+  const int e0 = lane8 * E;
+  float l[E], s[E], g[E];
+  load_logits<E>(a.logits, tok, mine, a.K, e0, l);
+  scores<float, E>(l, a.score, s);
+  uint32_t sel = 0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) g[j] = 0.f;
+  if (mine)
+    for (int i = 0; i < a.k; ++i) {
+      const int e = a.idx[(size_t)tok * a.k + i];
+      const float v = dw[(size_t)tok * a.k + i];
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (e == e0 + j) {
+          g[j] = v * a.factor;
+          sel |= 1u << j;
+        }
+    }
+  float sum = 0.f, dot = 0.f;  // of the chosen: s, s g
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    if ((sel >> j) & 1u) sum += s[j];
+    dot = fmaf(s[j], g[j], dot);
+  }
+  sum = sum8(sum);
+  dot = sum8(dot);
+  if (a.renorm) {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) g[j] = ((sel >> j) & 1u) ? (g[j] - dot * inv) * inv : 0.f;
+    dot = 0.f;  // sum of s g over the chosen: zero by construction
+  }
+  if (!mine) return;
+  float* out = dl + (size_t)tok * a.K + e0;
+  float r[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    r[j] = a.score == kScoreSigmoid ? s[j] * (1.f - s[j]) * g[j] : s[j] * (g[j] - dot);
+    if (!(l[j] > -INFINITY)) r[j] = 0.f;
+  }
+  if (a.K == kLanes * E) {
+    if constexpr (E >= 4) {
+#pragma unroll
+      for (int q = 0; q < E / 4; ++q)
+        st16(out + 4 * q, u32x4_t{__float_as_uint(r[4 * q]), __float_as_uint(r[4 * q + 1]), __float_as_uint(r[4 * q + 2]),
+                                  __float_as_uint(r[4 * q + 3])});
+    } else {
+      *reinterpret_cast<float2*>(out) = make_float2(r[0], r[1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (e0 + j < a.K) out[j] = r[j];
+  }
+}
+
+hipError_t launch_route_scores(const RouteScoresArgs& a, hipStream_t s) {
+  const dim3 grid((a.N + kTok * kWaves - 1) / (kTok * kWaves)), block(kWave * kWaves);
+  const size_t lds = a.n_group > 1 ? (size_t)kWaves * kTok * a.K * sizeof(double) : 0;
+  if (a.K <= 16) hipLaunchKernelGGL((route_scores_k<2>), grid, block, lds, s, a);
+  else if (a.K <= 32) hipLaunchKernelGGL((route_scores_k<4>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((route_scores_k<8>), grid, block, lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_scores_backward(const RouteScoresArgs& a, const float* dw, float* dl, hipStream_t s) {
+  const dim3 grid((a.N + kTok * kWaves - 1) / (kTok * kWaves)), block(kWave * kWaves);
+  if (a.K <= 16) hipLaunchKernelGGL((route_scores_bwd_k<2>), grid, block, 0, s, a, dw, dl);
+  else if (a.K <= 32) hipLaunchKernelGGL((route_scores_bwd_k<4>), grid, block, 0, s, a, dw, dl);
+  else hipLaunchKernelGGL((route_scores_bwd_k<8>), grid, block, 0, s, a, dw, dl);
+  return hipGetLastError();
+}
+
+}  // namespace molora
