@@ -188,6 +188,42 @@ int molora_attn_decode(const molora_kv_cache *cache, const molora_rows *q, const
                        const int32_t *lens, int window, int sinks, float scale, void *ws,
                        size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The synthetic decoder of molora_xf_forward in its serving form, over one
+ * paged cache per layer (d / 128 heads of 128 values, all of one page_size)
+ * that share table and lens.
+ * molora_xf_prefill runs the prompts that open n_seq sequences, N packed tokens
+ * with the rows [q_off[b], q_off[b+1]) of sequence b: every layer appends its
+ * keys and values to its cache and attends as molora_attn_forward does.
+ * lens[b] has to be the number of sequence b's rows.
+ * molora_xf_decode runs one new token per sequence: every layer appends it
+ * at position lens[b] - 1 and attends over the cache (molora_attn_decode).
+ * The projections, adapters, norms and rounding points are molora_xf_forward's,
+ * and so are d, f, layers, k and the routing (offsets, perm, perm_w, inv of
+ * molora_dispatch for the N, or n_seq, tokens).  window, sinks: as
+ * molora_attn_forward, the same for every layer.
+ *   x_in, x_out  device bf16 [N][d] (n_seq rows for molora_xf_decode; x_out
+ *                may equal x_in); rows outside every sequence are undefined
+ *   ws           molora_xf_serve_workspace() bytes for N tokens (n_seq for
+ *                molora_xf_decode), 256-byte aligned, no initial contents
+ * The layers' adapters have one rank (padded to a multiple of 16), else
+ * MOLORA_ENOTSUP.
+ * Errors as molora_xf_forward and the operators above.
+ * ------------------------------------------------------------------------ */
+int molora_xf_serve_workspace(int d, int f, int n_layers, const molora_xf_layer *layers,
+                              const molora_kv_cache *caches, int n_seq, int N, int table_width, int k,
+                              size_t *bytes);
+int molora_xf_prefill(int d, int f, int n_layers, const molora_xf_layer *layers,
+                      const molora_kv_cache *caches, int n_seq, int N, const int32_t *q_off,
+                      const int32_t *table, int table_width, const int32_t *lens, int window, int sinks,
+                      const void *x_in, void *x_out, int k, const int32_t *offsets, const int32_t *perm,
+                      const float *perm_w, const int32_t *inv, void *ws, size_t ws_bytes, void *stream);
+int molora_xf_decode(int d, int f, int n_layers, const molora_xf_layer *layers,
+                     const molora_kv_cache *caches, int n_seq, const int32_t *table, int table_width,
+                     const int32_t *lens, int window, int sinks, const void *x_in, void *x_out, int k,
+                     const int32_t *offsets, const int32_t *perm, const float *perm_w, const int32_t *inv,
+                     void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

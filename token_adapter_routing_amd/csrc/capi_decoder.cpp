@@ -4,6 +4,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "capi_internal.h"
 #include "decoder_launch.h"
@@ -310,6 +312,128 @@ int molora_attn_decode(const molora_kv_cache* cache, const molora_rows* q, const
   a.part = static_cast<float*>(ws);
   const hipError_t e = molora::launch_attn_decode(a, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attn_decode launch");
+}
+
+// The serving form's checks; on success *part is the decode attention's plan (single tokens).
+static int check_serve(int d, int f, int n_layers, const molora_xf_layer* layers, const molora_kv_cache* caches, int n_seq,
+                       int N, int table_width, int k, int* K, size_t* lora_bytes, int* paths, bool single,
+                       molora::DecodePlan* part) {
+  if (d <= 0 || f <= 0 || d % 128 != 0 || f % 128 != 0)
+    return fail(MOLORA_ENOTSUP, "d=%d and f=%d must be positive multiples of 128", d, f);
+  if (n_layers < 1 || n_layers > 1024 || layers == nullptr || caches == nullptr)
+    return fail(MOLORA_EINVAL, "n_layers=%d, or layers or caches NULL", n_layers);
+  if (n_seq < 0 || N < 0) return fail(MOLORA_EINVAL, "n_seq=%d, N=%d", n_seq, N);
+  const int heads = d / molora::kXfHeadDim;
+  if (N >= kMaxRows || (long long)N * std::max(d, f) >= (1ll << 31) || heads > 1024 ||
+      (long long)n_seq * heads >= kMaxRows || molora::attn_slots(N, n_seq, molora::kAttnQ) * heads >= (1ll << 31))
+    return fail(MOLORA_ENOTSUP, "batch of %d tokens in %d sequences too large", N, n_seq);
+  if (k < 1 || k > MOLORA_MAX_TOPK) return fail(MOLORA_ENOTSUP, "k=%d outside [1, %d]", k, MOLORA_MAX_TOPK);
+  for (int l = 0; l < n_layers; ++l) {
+    int rc = check_cache(&caches[l]);
+    if (rc == MOLORA_OK) rc = check_cache_ptrs(&caches[l]);
+    if (rc == MOLORA_OK) rc = check_table(&caches[l], n_seq, table_width);
+    if (rc != MOLORA_OK) return rc;
+    if (caches[l].head_dim != molora::kXfHeadDim || caches[l].n_kv_heads != heads)
+      return fail(MOLORA_EINVAL, "layer %d: the cache holds %d heads of %d, %d of %d needed", l, caches[l].n_kv_heads,
+                  caches[l].head_dim, heads, molora::kXfHeadDim);
+    if (caches[l].page_size != caches[0].page_size)
+      return fail(MOLORA_EINVAL, "layer %d: page_size %d differs from %d", l, caches[l].page_size, caches[0].page_size);
+  }
+  int first = -1;  // one resolved path per projection serves every layer
+  for (int l = 0; l < n_layers; ++l) {
+    if (layers[l].lora == nullptr) continue;
+    if (first < 0) first = l;
+    if (layers[l].lora->r_pad != layers[first].lora->r_pad)
+      return fail(MOLORA_ENOTSUP, "layers %d and %d: adapters of different (padded) rank", first, l);
+  }
+  *part = single ? molora::decode_plan(n_seq, heads, heads, molora::kXfHeadDim, caches[0].page_size, table_width)
+                 : molora::DecodePlan{};
+  return molora::xf_check_layers(d, f, n_layers, layers, std::max(N, 1), k, K, lora_bytes, paths);
+}
+
+int molora_xf_serve_workspace(int d, int f, int n_layers, const molora_xf_layer* layers, const molora_kv_cache* caches,
+                              int n_seq, int N, int table_width, int k, size_t* bytes) {
+  if (bytes == nullptr) return fail(MOLORA_EINVAL, "bytes is NULL");
+  int K = 0;
+  size_t lb = 0;
+  molora::DecodePlan part{};
+  const int rc = check_serve(d, f, n_layers, layers, caches, n_seq, N, table_width, k, &K, &lb, nullptr, true, &part);
+  if (rc != MOLORA_OK) return rc;
+  *bytes = molora::xf_serve_plan(N, d, f, lb, part.total).total;
+  return ok();
+}
+
+static int serve(int d, int f, int n_layers, const molora_xf_layer* layers, const molora_kv_cache* caches, int n_seq,
+                 int N, const int32_t* q_off, const int32_t* table, int table_width, const int32_t* lens, int window,
+                 int sinks, const void* x_in, void* x_out, int k, const int32_t* offsets, const int32_t* perm,
+                 const float* perm_w, const int32_t* inv, void* ws, size_t ws_bytes, void* stream, bool single) {
+  int K = 0, paths[4] = {0, 0, 0, 0};
+  size_t lb = 0;
+  molora::DecodePlan part{};
+  int rc = check_serve(d, f, n_layers, layers, caches, n_seq, N, table_width, k, &K, &lb, paths, single, &part);
+  if (rc != MOLORA_OK) return rc;
+  if ((rc = check_mask(window, sinks, 1.f)) != MOLORA_OK) return rc;
+  if (N == 0) return ok();
+  if (n_seq == 0) return fail(MOLORA_EINVAL, "%d tokens in no sequence", N);
+  if (x_in == nullptr || x_out == nullptr || !aligned(x_in, 16) || !aligned(x_out, 16))
+    return fail(MOLORA_EINVAL, "x_in or x_out NULL or not 16-byte aligned");
+  if (table == nullptr || lens == nullptr || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_off, 4) ||
+      (!single && q_off == nullptr))
+    return fail(MOLORA_EINVAL, "table, lens or q_off NULL or misaligned");
+  if (table_width == 0) return fail(MOLORA_EINVAL, "table_width is 0");
+  if (K > 0 && (offsets == nullptr || perm == nullptr || perm_w == nullptr || inv == nullptr || !aligned(offsets, 4) ||
+                !aligned(perm, 4) || !aligned(perm_w, 4) || !aligned(inv, 4)))
+    return fail(MOLORA_EINVAL, "offsets, perm, perm_w and inv are required, 4-byte aligned, with LoRA layers");
+  const size_t need = molora::xf_serve_plan(N, d, f, lb, part.total).total;
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(MOLORA_ENOSPC, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need, ws_bytes);
+  std::unique_ptr<molora::XfLayerDev[]> dev(new (std::nothrow) molora::XfLayerDev[n_layers]);
+  std::unique_ptr<molora::KvCacheDev[]> cd(new (std::nothrow) molora::KvCacheDev[n_layers]);
+  if (dev == nullptr || cd == nullptr) return fail(MOLORA_EHIP, "out of host memory");
+  molora::xf_layers_dev(n_layers, layers, dev.get());
+  for (int l = 0; l < n_layers; ++l) cd[l] = cache_dev(&caches[l]);
+  const char* what = "";
+  molora::XfServeLaunch v{};
+  molora::XfLaunch& a = v.xf;
+  a.d = d; a.f = f; a.n_seq = N; a.seq_len = 1; a.n_layers = n_layers; a.K = K; a.k = k;
+  a.eps = 1e-6f;
+  a.layers = dev.get();
+  a.x_in = static_cast<const uint16_t*>(x_in);
+  a.x_out = static_cast<uint16_t*>(x_out);
+  a.offsets = offsets; a.perm = perm; a.perm_w = perm_w; a.inv = inv;
+  a.path_qkv = paths[0]; a.path_o = paths[1]; a.path_gu = paths[2]; a.path_down = paths[3];
+  a.lora_bytes = lb;
+  a.ws = static_cast<char*>(ws);
+  a.what = &what;
+  v.caches = cd.get();
+  v.n_seq = n_seq;
+  v.q_off = single ? nullptr : q_off;
+  v.table = table;
+  v.width = table_width;
+  v.lens = lens;
+  v.window = std::min(window, kMaxWindow);
+  v.sinks = sinks;
+  v.splits = part.splits;
+  v.part_bytes = part.total;
+  const hipError_t e = molora::launch_xf_serve(v, stream_of(stream));
+  if (e != hipSuccess) return fail(MOLORA_EHIP, "decoder serving (%s): %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+int molora_xf_prefill(int d, int f, int n_layers, const molora_xf_layer* layers, const molora_kv_cache* caches, int n_seq,
+                      int N, const int32_t* q_off, const int32_t* table, int table_width, const int32_t* lens, int window,
+                      int sinks, const void* x_in, void* x_out, int k, const int32_t* offsets, const int32_t* perm,
+                      const float* perm_w, const int32_t* inv, void* ws, size_t ws_bytes, void* stream) {
+  return serve(d, f, n_layers, layers, caches, n_seq, N, q_off, table, table_width, lens, window, sinks, x_in, x_out, k,
+               offsets, perm, perm_w, inv, ws, ws_bytes, stream, false);
+}
+
+int molora_xf_decode(int d, int f, int n_layers, const molora_xf_layer* layers, const molora_kv_cache* caches, int n_seq,
+                     const int32_t* table, int table_width, const int32_t* lens, int window, int sinks, const void* x_in,
+                     void* x_out, int k, const int32_t* offsets, const int32_t* perm, const float* perm_w,
+                     const int32_t* inv, void* ws, size_t ws_bytes, void* stream) {
+  return serve(d, f, n_layers, layers, caches, n_seq, n_seq, nullptr, table, table_width, lens, window, sinks, x_in,
+               x_out, k, offsets, perm, perm_w, inv, ws, ws_bytes, stream, true);
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "decoder_plan.h"
+#include "molora_launch.h"
 
 namespace molora {
 
@@ -77,5 +78,20 @@ struct DecodeArgs {
   float* part;  // decode_plan, splits > 1
 };
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);
+
+// The decoder over a paged cache per layer (xfmr.cpp): xf holds n_seq * seq_len = the new tokens.
+struct XfServeLaunch {
+  XfLaunch xf;
+  const KvCacheDev* caches;  // [n_layers]
+  int n_seq;
+  const int32_t* q_off;  // prompts; NULL: one token per sequence
+  const int32_t* table;
+  int width;
+  const int32_t* lens;
+  int window, sinks;
+  int splits;         // decode_plan, single tokens
+  size_t part_bytes;  // its workspace
+};
+hipError_t launch_xf_serve(const XfServeLaunch& a, hipStream_t s);
 
 }  // namespace molora

@@ -22,4 +22,26 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
   return p;
 }
 
+XfServePlan xf_serve_plan(int N, int d, int f, size_t lora_bytes, size_t part_bytes) {
+  XfServePlan p{};
+  const size_t nd = align256((size_t)N * d * sizeof(uint16_t)), nf = align256((size_t)N * f * sizeof(uint16_t));
+  size_t off = 0;
+  for (size_t* at : {&p.h_off, &p.q_off, &p.k_off, &p.v_off, &p.att_off, &p.o_off}) {
+    *at = off;
+    off += nd;
+  }
+  for (size_t* at : {&p.g_off, &p.u_off}) {
+    *at = off;
+    off += nf;
+  }
+  p.part_off = off;
+  off += align256(part_bytes);
+  p.lora_off = off;
+  off += align256(lora_bytes);
+  p.blas_off = off;
+  p.blas_bytes = kXfBlasBytes;
+  p.total = off + p.blas_bytes;
+  return p;
+}
+
 }  // namespace molora

@@ -41,4 +41,13 @@ MOLORA_HD inline int decode_blocks_per_split(int blocks, int splits) {
   return per < kDecMinBlocks ? kDecMinBlocks : per;
 }
 
+// ---- the synthetic decoder's serving form over N new tokens: the activations of xf_plan without
+// scores and probabilities, the decode attention's parts, the applies' and the GEMM library's
+// workspaces.
+struct XfServePlan {
+  size_t h_off, q_off, k_off, v_off, att_off, o_off, g_off, u_off;
+  size_t part_off, lora_off, blas_off, blas_bytes, total;
+};
+XfServePlan xf_serve_plan(int N, int d, int f, size_t lora_bytes, size_t part_bytes);
+
 }  // namespace molora

@@ -24,6 +24,7 @@
 #include <map>
 #include <mutex>
 
+#include "decoder_launch.h"
 #include "molora_launch.h"
 
 namespace molora {
@@ -80,34 +81,20 @@ ApplyLaunch lora_launch(const XfLaunch& a, const XfLayerDev& L, int t, const uin
   return p;
 }
 
-}  // namespace
-
-hipError_t launch_xf_forward(const XfLaunch& a, hipStream_t s) {
-  std::lock_guard<std::mutex> lock(g_blas_mu);
-  rocblas_handle h = blas_for_current_device(a.what);
+// The library's handle for the current device on stream s, its workspace at blas_ws; the caller
+// holds g_blas_mu.
+hipError_t blas_on_stream(hipStream_t s, char* blas_ws, size_t blas_bytes, rocblas_handle* out, const char** what) {
+  rocblas_handle h = blas_for_current_device(what);
   if (h == nullptr) return hipErrorUnknown;
-  const XfPlan p = xf_plan(a.n_seq, a.seq_len, a.d, a.f, a.lora_bytes);
   if (rocblas_set_stream(h, s) != rocblas_status_success ||
-      rocblas_set_workspace(h, a.ws + p.blas_off, p.blas_bytes) != rocblas_status_success) {
-    *a.what = "rocblas stream / workspace";
+      rocblas_set_workspace(h, blas_ws, blas_bytes) != rocblas_status_success) {
+    *what = "rocblas stream / workspace";
     return hipErrorUnknown;
   }
-  auto P = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
-  uint16_t* hb = P(p.h_off);
-  uint16_t* q = P(p.q_off);
-  uint16_t* k = P(p.k_off);
-  uint16_t* v = P(p.v_off);
-  uint16_t* att = P(p.att_off);
-  uint16_t* o = P(p.o_off);
-  uint16_t* g = P(p.g_off);
-  uint16_t* u = P(p.u_off);
-  float* S = reinterpret_cast<float*>(a.ws + p.s_off);
-  uint16_t* Pr = P(p.p_off);
-  char* lws = a.ws + p.lora_off;
-  const int N = a.n_seq * a.seq_len, d = a.d, f = a.f, T = a.seq_len, H = d / kXfHeadDim;
-  const long long nd = (long long)N * d, nf = (long long)N * f;
-  const float qk_scale = 1.f / std::sqrt((float)kXfHeadDim), one = 1.f, zero = 0.f;
-  hipError_t err = hipSuccess;
+  *out = h;
+  return hipSuccess;
+}
+
 #define XF_HIP(call, name)      \
   if ((err = (call)) != hipSuccess) { \
     *a.what = name;             \
@@ -118,25 +105,84 @@ hipError_t launch_xf_forward(const XfLaunch& a, hipStream_t s) {
     *a.what = name;                                     \
     return hipErrorUnknown;                             \
   }
+
+// Activations of one layer (bf16) and the applies' workspace.
+struct XfBufs {
+  uint16_t *h, *q, *k, *v, *att, *o, *g, *u;
+  char* lora;
+};
+
+// The layers over a.n_seq * a.seq_len tokens; attention(l) enqueues layer l's attention from b.q, b.k
+// and b.v into b.att.
+template <typename Attention>
+hipError_t xf_layers(const XfLaunch& a, rocblas_handle h, const XfBufs& b, Attention attention, hipStream_t s) {
+  const int N = a.n_seq * a.seq_len, d = a.d, f = a.f;
+  const long long nd = (long long)N * d, nf = (long long)N * f;
+  hipError_t err = hipSuccess;
   const uint16_t* cur = a.x_in;
   for (int l = 0; l < a.n_layers; ++l) {
     const XfLayerDev& L = a.layers[l];
-    XF_HIP(launch_xf_rmsnorm(cur, L.norm1, hb, N, d, a.eps, s), "rmsnorm");
-    XF_BLAS(linear(h, hb, L.W[kXfQ], q, N, d, d), "q projection");
-    XF_BLAS(linear(h, hb, L.W[kXfK], k, N, d, d), "k projection");
-    XF_BLAS(linear(h, hb, L.W[kXfV], v, N, d, d), "v projection");
+    XF_HIP(launch_xf_rmsnorm(cur, L.norm1, b.h, N, d, a.eps, s), "rmsnorm");
+    XF_BLAS(linear(h, b.h, L.W[kXfQ], b.q, N, d, d), "q projection");
+    XF_BLAS(linear(h, b.h, L.W[kXfK], b.k, N, d, d), "k projection");
+    XF_BLAS(linear(h, b.h, L.W[kXfV], b.v, N, d, d), "v projection");
     if (L.lora) {
-      ApplyLaunch m[3] = {lora_launch(a, L, kXfQ, hb, q, a.path_qkv, lws), lora_launch(a, L, kXfK, hb, k, a.path_qkv, lws),
-                          lora_launch(a, L, kXfV, hb, v, a.path_qkv, lws)};
+      ApplyLaunch m[3] = {lora_launch(a, L, kXfQ, b.h, b.q, a.path_qkv, b.lora),
+                          lora_launch(a, L, kXfK, b.h, b.k, a.path_qkv, b.lora),
+                          lora_launch(a, L, kXfV, b.h, b.v, a.path_qkv, b.lora)};
       XF_HIP(launch_apply_multi(m, 3, s), "q/k/v LoRA");
     }
+    if ((err = attention(l)) != hipSuccess) return err;
+    XF_BLAS(linear(h, b.att, L.W[kXfO], b.o, N, d, d), "o projection");
+    if (L.lora) {
+      const ApplyLaunch m = lora_launch(a, L, kXfO, b.att, b.o, a.path_o, b.lora);
+      XF_HIP(launch_apply(m, s), "o LoRA");
+    }
+    XF_HIP(launch_xf_add(cur, b.o, a.x_out, nd, s), "residual");
+    cur = a.x_out;
+    XF_HIP(launch_xf_rmsnorm(cur, L.norm2, b.h, N, d, a.eps, s), "rmsnorm");
+    XF_BLAS(linear(h, b.h, L.W[kXfGate], b.g, N, d, f), "gate projection");
+    XF_BLAS(linear(h, b.h, L.W[kXfUp], b.u, N, d, f), "up projection");
+    if (L.lora) {
+      ApplyLaunch m[2] = {lora_launch(a, L, kXfGate, b.h, b.g, a.path_gu, b.lora),
+                          lora_launch(a, L, kXfUp, b.h, b.u, a.path_gu, b.lora)};
+      XF_HIP(launch_apply_multi(m, 2, s), "gate/up LoRA");
+    }
+    XF_HIP(launch_xf_swiglu(b.g, b.u, nf, s), "swiglu");
+    XF_BLAS(linear(h, b.g, L.W[kXfDown], b.o, N, f, d), "down projection");
+    if (L.lora) {
+      const ApplyLaunch m = lora_launch(a, L, kXfDown, b.g, b.o, a.path_down, b.lora);
+      XF_HIP(launch_apply(m, s), "down LoRA");
+    }
+    XF_HIP(launch_xf_add(cur, b.o, a.x_out, nd, s), "residual");
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_xf_forward(const XfLaunch& a, hipStream_t s) {
+  std::lock_guard<std::mutex> lock(g_blas_mu);
+  const XfPlan p = xf_plan(a.n_seq, a.seq_len, a.d, a.f, a.lora_bytes);
+  rocblas_handle h = nullptr;
+  const hipError_t e = blas_on_stream(s, a.ws + p.blas_off, p.blas_bytes, &h, a.what);
+  if (e != hipSuccess) return e;
+  auto P = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
+  const XfBufs buf{P(p.h_off), P(p.q_off), P(p.k_off), P(p.v_off), P(p.att_off),
+                   P(p.o_off), P(p.g_off), P(p.u_off), a.ws + p.lora_off};
+  float* S = reinterpret_cast<float*>(a.ws + p.s_off);
+  uint16_t* Pr = P(p.p_off);
+  const int d = a.d, T = a.seq_len, H = d / kXfHeadDim;
+  const float qk_scale = 1.f / std::sqrt((float)kXfHeadDim), one = 1.f, zero = 0.f;
+  auto attention = [&](int) -> hipError_t {
+    hipError_t err = hipSuccess;
     for (int b = 0; b < a.n_seq; ++b) {
       const size_t tok0 = (size_t)b * T * d;
       float* Sb = S + (size_t)b * H * T * T;
       uint16_t* Pb = Pr + (size_t)b * H * T * T;
       // column-major S^T[j][i] = k_j . q_i, i.e. row-major S[i][j], per head (stride 128)
       XF_BLAS(rocblas_gemm_strided_batched_ex(h, rocblas_operation_transpose, rocblas_operation_none, T, T, kXfHeadDim,
-                                              &qk_scale, k + tok0, rocblas_datatype_bf16_r, d, kXfHeadDim, q + tok0,
+                                              &qk_scale, buf.k + tok0, rocblas_datatype_bf16_r, d, kXfHeadDim, buf.q + tok0,
                                               rocblas_datatype_bf16_r, d, kXfHeadDim, &zero, Sb,
                                               rocblas_datatype_f32_r, T, (rocblas_stride)T * T, Sb,
                                               rocblas_datatype_f32_r, T, (rocblas_stride)T * T, H,
@@ -145,39 +191,75 @@ hipError_t launch_xf_forward(const XfLaunch& a, hipStream_t s) {
       XF_HIP(launch_xf_softmax_causal(Sb, Pb, T, (long long)H * T, s), "softmax");
       // column-major att^T[c][i] = sum_j v_j[c] P[i][j]
       XF_BLAS(rocblas_gemm_strided_batched_ex(h, rocblas_operation_none, rocblas_operation_none, kXfHeadDim, T, T, &one,
-                                              v + tok0, rocblas_datatype_bf16_r, d, kXfHeadDim, Pb,
-                                              rocblas_datatype_bf16_r, T, (rocblas_stride)T * T, &zero, att + tok0,
-                                              rocblas_datatype_bf16_r, d, kXfHeadDim, att + tok0,
+                                              buf.v + tok0, rocblas_datatype_bf16_r, d, kXfHeadDim, Pb,
+                                              rocblas_datatype_bf16_r, T, (rocblas_stride)T * T, &zero, buf.att + tok0,
+                                              rocblas_datatype_bf16_r, d, kXfHeadDim, buf.att + tok0,
                                               rocblas_datatype_bf16_r, d, kXfHeadDim, H, rocblas_datatype_f32_r,
                                               rocblas_gemm_algo_standard, 0, 0),
               "attention values");
     }
-    XF_BLAS(linear(h, att, L.W[kXfO], o, N, d, d), "o projection");
-    if (L.lora) {
-      const ApplyLaunch m = lora_launch(a, L, kXfO, att, o, a.path_o, lws);
-      XF_HIP(launch_apply(m, s), "o LoRA");
+    return hipSuccess;
+  };
+  return xf_layers(a, h, buf, attention, s);
+}
+
+// The serving form: the new tokens' keys and values go into each layer's cache; prompts then attend to
+// each other's packed rows, single tokens to the cache.
+hipError_t launch_xf_serve(const XfServeLaunch& v, hipStream_t s) {
+  std::lock_guard<std::mutex> lock(g_blas_mu);
+  const XfLaunch& a = v.xf;
+  const int N = a.n_seq * a.seq_len, d = a.d, H = d / kXfHeadDim;
+  const XfServePlan p = xf_serve_plan(N, d, a.f, a.lora_bytes, v.part_bytes);
+  rocblas_handle h = nullptr;
+  const hipError_t e = blas_on_stream(s, a.ws + p.blas_off, p.blas_bytes, &h, a.what);
+  if (e != hipSuccess) return e;
+  auto P = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
+  const XfBufs buf{P(p.h_off), P(p.q_off), P(p.k_off), P(p.v_off), P(p.att_off),
+                   P(p.o_off), P(p.g_off), P(p.u_off), a.ws + p.lora_off};
+  auto rows = [&](uint16_t* x) { return Rows{x, d, kXfHeadDim}; };
+  const float scale = 1.f / std::sqrt((float)kXfHeadDim);
+  auto attention = [&](int l) -> hipError_t {
+    hipError_t err = hipSuccess;
+    const KvAppendArgs ap{v.caches[l], rows(buf.k), rows(buf.v), N, v.n_seq, v.q_off, v.table, v.width, v.lens};
+    XF_HIP(launch_kv_append(ap, s), "cache append");
+    if (v.q_off != nullptr) {
+      AttnArgs t{};
+      t.q = rows(buf.q);
+      t.k = rows(buf.k);
+      t.v = rows(buf.v);
+      t.o = rows(buf.att);
+      t.q_off = t.kv_off = v.q_off;
+      t.n_seq = v.n_seq;
+      t.Hq = t.Hkv = H;
+      t.D = kXfHeadDim;
+      t.Tq = t.Tkv = N;
+      t.window = v.window;
+      t.sinks = v.sinks;
+      t.scale = scale;
+      XF_HIP(launch_attn_forward(t, s), "attention");
+    } else {
+      DecodeArgs t{};
+      t.c = v.caches[l];
+      t.q = rows(buf.q);
+      t.o = rows(buf.att);
+      t.n_seq = v.n_seq;
+      t.Hq = H;
+      t.table = v.table;
+      t.width = v.width;
+      t.lens = v.lens;
+      t.window = v.window;
+      t.sinks = v.sinks;
+      t.scale = scale;
+      t.splits = v.splits;
+      t.part = reinterpret_cast<float*>(a.ws + p.part_off);
+      XF_HIP(launch_attn_decode(t, s), "attention over the cache");
     }
-    XF_HIP(launch_xf_add(cur, o, a.x_out, nd, s), "residual");
-    cur = a.x_out;
-    XF_HIP(launch_xf_rmsnorm(cur, L.norm2, hb, N, d, a.eps, s), "rmsnorm");
-    XF_BLAS(linear(h, hb, L.W[kXfGate], g, N, d, f), "gate projection");
-    XF_BLAS(linear(h, hb, L.W[kXfUp], u, N, d, f), "up projection");
-    if (L.lora) {
-      ApplyLaunch m[2] = {lora_launch(a, L, kXfGate, hb, g, a.path_gu, lws),
-                          lora_launch(a, L, kXfUp, hb, u, a.path_gu, lws)};
-      XF_HIP(launch_apply_multi(m, 2, s), "gate/up LoRA");
-    }
-    XF_HIP(launch_xf_swiglu(g, u, nf, s), "swiglu");
-    XF_BLAS(linear(h, g, L.W[kXfDown], o, N, f, d), "down projection");
-    if (L.lora) {
-      const ApplyLaunch m = lora_launch(a, L, kXfDown, g, o, a.path_down, lws);
-      XF_HIP(launch_apply(m, s), "down LoRA");
-    }
-    XF_HIP(launch_xf_add(cur, o, a.x_out, nd, s), "residual");
-  }
+    return hipSuccess;
+  };
+  return xf_layers(a, h, buf, attention, s);
+}
+
 #undef XF_HIP
 #undef XF_BLAS
-  return hipSuccess;
-}
 
 }  // namespace molora

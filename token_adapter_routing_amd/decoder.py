@@ -45,6 +45,11 @@ _SIGS = {
     "molora_attn_decode_workspace": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_p]),
     "molora_attn_decode": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i, _c_i, _c_f, _c_p, _c_sz,
                                   _c_p]),
+    "molora_xf_serve_workspace": (_c_i, [_c_i, _c_i, _c_i, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p]),
+    "molora_xf_prefill": (_c_i, [_c_i, _c_i, _c_i, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_i, _c_p, _c_i, _c_i,  # .. sinks
+                                 _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "molora_xf_decode": (_c_i, [_c_i, _c_i, _c_i, _c_p, _c_p, _c_i, _c_p, _c_i, _c_p, _c_i, _c_i,  # .. sinks
+                                _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
 }
 _lib = None
 
@@ -311,3 +316,65 @@ def molora_attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, len
         _flat(table, torch.int32, (n, width), "table"), width, _flat(lens, torch.int32, (n,), "lens"), int(window),
         int(sinks), 1.0 / math.sqrt(D) if scale is None else float(scale), wp, wn, _stream()))
     return out, lse
+
+
+# ----------------------------------------------------------------------------------- the decoder, serving
+
+def _caches(model, caches):
+    if len(caches) != len(model.layers):
+        raise ValueError(f"{len(model.layers)} layers need as many caches, got {len(caches)}")
+    return (MoloraKvCache * len(caches))(*[c._c for c in caches])
+
+
+def molora_xf_serve_workspace(model, caches, n_seq: int, N: int, table_width: int, k: int = 1) -> int:
+    n = _c_sz()
+    _check(_library().molora_xf_serve_workspace(model.d, model.f, len(model.layers), model._arr, _caches(model, caches),
+                                                int(n_seq), int(N), int(table_width), int(k), ctypes.byref(n)))
+    return n.value
+
+
+def _serve(model, caches, x, q_off, table, lens, window, sinks, route, k, out, ws):
+    N, (n, width) = x.shape[0], table.shape
+    if q_off is None and N != n:
+        raise ValueError(f"one token per sequence: {N} rows for {n} sequences")
+    if out is None:
+        out = torch.empty_like(x)
+    arr = _caches(model, caches)
+    lib = _library()
+    need = _c_sz()
+    _check(lib.molora_xf_serve_workspace(model.d, model.f, len(model.layers), model._arr, arr, n, N, width, int(k),
+                                         ctypes.byref(need)))
+    wp, wn, ws = _workspace(ws, need.value, x.device)
+    K = next((L["lora"].K for L in model.layers if L.get("lora") is not None), 0)
+    r = (None,) * 4
+    if route is not None:
+        P = N * int(k)
+        r = tuple(_flat(t[:P] if name != "offsets" else t, dt, (K + 1,) if name == "offsets" else (P,), name)
+                  for t, dt, name in zip(route, (torch.int32, torch.int32, torch.float32, torch.int32),
+                                         ("offsets", "perm", "perm_w", "inv")))
+    head = (model.d, model.f, len(model.layers), model._arr, arr, n)
+    tail = (_flat(table, torch.int32, (n, width), "table"), width, _flat(lens, torch.int32, (n,), "lens"), int(window),
+            int(sinks), _flat(x, torch.bfloat16, (N, model.d), "x"), _flat(out, torch.bfloat16, (N, model.d), "out"), int(k),
+            *r, wp, wn, _stream())
+    if q_off is None:
+        _check(lib.molora_xf_decode(*head, *tail))
+    else:
+        _check(lib.molora_xf_prefill(*head, N, _flat(q_off, torch.int32, (n + 1,), "q_off"), *tail))
+    return out
+
+
+@_on_stream
+def molora_xf_prefill(model, caches, x: torch.Tensor, q_off: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      window: int = 0, sinks: int = 0, route=None, k: int = 1, out: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None):
+    """The decoder (an XfModel) over prompts that open their sequences: x bf16 [N][d] packed rows, one KvCache
+    per layer, route = (offsets, perm, perm_w, inv) of molora_dispatch for the N tokens."""
+    return _serve(model, caches, x, q_off, table, lens, window, sinks, route, k, out, ws)
+
+
+@_on_stream
+def molora_xf_decode(model, caches, x: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, window: int = 0,
+                     sinks: int = 0, route=None, k: int = 1, out: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None):
+    """The decoder over one new token per sequence, x bf16 [n_seq][d]; lens with the new tokens."""
+    return _serve(model, caches, x, None, table, lens, window, sinks, route, k, out, ws)
