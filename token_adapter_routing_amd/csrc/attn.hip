@@ -38,44 +38,69 @@ struct Tile {
   static __device__ __forceinline__ int off(int row, int piece) { return row * kRow + ((piece ^ swz(row)) << 4); }
 };
 
-// Copies ROWS rows of a packed tensor into an LDS tile by way of registers: load() requests, store()
-// writes.  Rows past `last` repeat row `last`.
+// Asynchronous copy of ROWS rows of a packed tensor into an LDS tile, straight from global memory: an
+// instruction fills 1 KiB of LDS in lane order, so the lanes pick the global pieces that the tile's
+// permutation puts there.  Rows past `last` repeat row `last`.  The data is there after
+// tiles_ready().
 template <int D, int ROWS>
-struct Stage {
-  static constexpr int kN = ROWS * Tile<D>::kPieces / 256;
-  u32x4_t r[kN];
-  __device__ __forceinline__ void load(const uint16_t* base, uint32_t stride, int row0, int last, int tid) {
-    const uint16_t* p = base + (long long)row0 * stride;
+struct Fetch {
+  static constexpr int kRows = 1024 / Tile<D>::kRow;    // rows per instruction
+  static constexpr int kN = ROWS / kRows / 4;           // instructions per wave
+  uint32_t row[kN], col[kN];
+  __device__ __forceinline__ void init(int lane, int wave) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int id = tid + 256 * i, row = id / Tile<D>::kPieces, c = id % Tile<D>::kPieces;
-      r[i] = ld16(p + (uint32_t)(min(row, last - row0) * stride + c * 8));
+      const int r = (4 * i + wave) * kRows + lane / Tile<D>::kPieces;
+      row[i] = r;
+      col[i] = 16 * ((lane % Tile<D>::kPieces) ^ Tile<D>::swz(r));
     }
   }
-  __device__ __forceinline__ void store(char* lds, int tid) const {
+  // stride in bytes
+  __device__ __forceinline__ void operator()(char* __restrict__ lds, const uint16_t* base, long long stride, int row0,
+                                             int last, int wave) const {
+    const char* p = reinterpret_cast<const char*>(base) + row0 * stride;
+    const uint32_t left = last - row0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int id = tid + 256 * i, row = id / Tile<D>::kPieces, c = id % Tile<D>::kPieces;
-      st16(lds + Tile<D>::off(row, c), r[i]);
-    }
+    for (int i = 0; i < kN; ++i)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(p + (min(row[i], left) * (uint32_t)stride + col[i])),
+          (__attribute__((address_space(3))) void*)(lds + (4 * i + wave) * 1024), 16, 0, 0);
   }
 };
 
-// Left operand (rows down): row `row` of the tile, values 16 st + 8 h .. + 7.
+// This wave's copies into LDS have arrived, then everyone's.
+__device__ __forceinline__ void tiles_ready() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+// Lane's places in any tile.  The permutation XORs row bits 0..3 into the piece, so neighbouring
+// operands are an XOR and a constant apart: row operands st differ in piece bits 1.., column operands
+// in piece bits 2.. (mb) and, eight rows on, in piece bit 1.
+struct LaneOff {
+  uint32_t row, col;
+};
 template <int D>
-__device__ __forceinline__ bf16x8_t row_frag(const char* lds, int row, int st, int h) {
-  return as_bf16x8(ld16(lds + Tile<D>::off(row, 2 * st + h)));
+__device__ __forceinline__ LaneOff lane_off(int lane) {
+  const int h = lane >> 5, q = lane & 15, c = (lane & 16) + 4 * (q & 3);
+  return {(uint32_t)Tile<D>::off(lane & 31, h), (uint32_t)(Tile<D>::off(4 * h + (q >> 2), c >> 3) + (c & 4) * 2)};
+}
+
+// Left operand (rows down): rows row0 + lane % 32 (row0 a multiple of 16), values 16 st + 8 h .. + 7.
+template <int D>
+__device__ __forceinline__ bf16x8_t row_frag(const char* lds, LaneOff o, int row0, int st) {
+  return as_bf16x8(ld16(lds + ((o.row ^ (st << 5)) + row0 * Tile<D>::kRow)));
 }
 
 // Left operand (columns down): column 32 mb + lane % 32 of the tile; k-slots 0..3 are rows
-// row0 + 4 h + 0..3, k-slots 4..7 rows row0 + 8 + 4 h + 0..3, the order in which a 32x32 result
-// holds its rows.  Each group of 16 lanes reads a 4 x 16 block and gets its columns.
+// row0 + 4 h + 0..3 (row0 a multiple of 16), k-slots 4..7 rows row0 + 8 + 4 h + 0..3, the order in
+// which a 32x32 result holds its rows.  Each group of 16 lanes reads a 4 x 16 block and gets its
+// columns.
 template <int D>
-__device__ __forceinline__ bf16x8_t col_frag(const char* lds, int row0, int mb, int lane) {
+__device__ __forceinline__ bf16x8_t col_frag(const char* lds, LaneOff o, int row0, int mb) {
   typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-  const int h = lane >> 5, q = lane & 15, col = 32 * mb + (lane & 16) + 4 * (q & 3), row = row0 + 4 * h + (q >> 2);
-  const char* a = lds + Tile<D>::off(row, col >> 3) + (col & 4) * 2;
-  const char* b = lds + Tile<D>::off(row + 8, col >> 3) + (col & 4) * 2;
+  const char* a = lds + ((o.col ^ (mb << 6)) + row0 * Tile<D>::kRow);
+  const char* b = lds + ((o.col ^ (mb << 6) ^ 32) + (row0 + 8) * Tile<D>::kRow);
   union {
     s16x4_t s[2];
     bf16x8_t v;
@@ -173,8 +198,8 @@ __device__ __forceinline__ void store_rows(uint16_t* row, const f32x16_t* acc, f
 // A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int kTileB = kBN * Tile<D>::kRow;
+  __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const Place pl = place(a, slots);
@@ -198,29 +223,23 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
   for (int mb = 0; mb < D / 32; ++mb) o[mb] = f32x16_t{};
   const float c = a.scale * kLog2e;  // the softmax in base 2
   float mx = -INFINITY, sum = 0.f;   // reference maximum of c s; the lane's part of the sum
-  Stage<D, kBN> sk, sv;
-  if (kt.n > 0) {
-    sk.load(kb, (uint32_t)a.k.token, kt.at(0), t.Lk - 1, tid);
-    sv.load(vb, (uint32_t)a.v.token, kt.at(0), t.Lk - 1, tid);
-    sk.store(lds, tid);
-    sv.store(lds + 2 * kTileB, tid);
-  }
-  __syncthreads();
-  for (int it = 0; it < kt.n; ++it) {
+  Fetch<D, kBN> fetch;
+  fetch.init(lane, wave);
+  const LaneOff lo = lane_off<D>(lane);
+  const long long ks = 2 * a.k.token, vs = 2 * a.v.token;
+  auto step = [&](int it, const char* __restrict__ K, const char* __restrict__ V, char* __restrict__ nextK,
+                  char* __restrict__ nextV) {
     const int j0 = kt.at(it);
-    const char* K = lds + (it & 1) * kTileB;
-    const char* V = lds + (2 + (it & 1)) * kTileB;
-    const bool more = it + 1 < kt.n;
-    if (more) {
-      sk.load(kb, (uint32_t)a.k.token, kt.at(it + 1), t.Lk - 1, tid);
-      sv.load(vb, (uint32_t)a.v.token, kt.at(it + 1), t.Lk - 1, tid);
+    if (it + 1 < kt.n) {
+      fetch(nextK, kb, ks, kt.at(it + 1), t.Lk - 1, wave);
+      fetch(nextV, vb, vs, kt.at(it + 1), t.Lk - 1, wave);
     }
     if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
       f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
 #pragma unroll
       for (int st = 0; st < D / 16; ++st)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) s[b] = mfma32x32x16(row_frag<D>(K, 32 * b + n, st, h), q[st], s[b]);
+        for (int b = 0; b < 2; ++b) s[b] = mfma32x32x16(row_frag<D>(K, lo, 32 * b, st), q[st], s[b]);
       if (!sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -257,14 +276,19 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
       for (int st = 0; st < kBN / 16; ++st) {
         const bf16x8_t pf = acc_frag(s[st >> 1], st & 1);
 #pragma unroll
-        for (int mb = 0; mb < D / 32; ++mb) o[mb] = mfma32x32x16(col_frag<D>(V, 16 * st, mb, lane), pf, o[mb]);
+        for (int mb = 0; mb < D / 32; ++mb) o[mb] = mfma32x32x16(col_frag<D>(V, lo, 16 * st, mb), pf, o[mb]);
       }
     }
-    if (more) {
-      sk.store(lds + ((it + 1) & 1) * kTileB, tid);
-      sv.store(lds + (2 + ((it + 1) & 1)) * kTileB, tid);
-    }
-    __syncthreads();
+    tiles_ready();
+  };
+  if (kt.n > 0) {
+    fetch(ldsK0, kb, ks, kt.at(0), t.Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(0), t.Lk - 1, wave);
+  }
+  tiles_ready();
+  for (int it = 0; it < kt.n; it += 2) {
+    step(it, ldsK0, ldsV0, ldsK1, ldsV1);
+    if (it + 1 < kt.n) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   sum += __shfl_xor(sum, 32, kWave);
   if (r0 + n > last) return;
@@ -277,8 +301,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
 // the keys as the forward does.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long long slots) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int kTileB = kBN * Tile<D>::kRow;
+  __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
@@ -314,27 +338,24 @@ __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long lon
   }
   const size_t stat = (size_t)pl.hq * a.Tq + t.q0 + r;
   const float lse2 = a.lse[stat] * kLog2e;
-  if (h == 0 && r0 + n <= last) b.delta[stat] = delta;
+  if (h == 0 && r0 + n <= last) {
+    b.lse2[stat] = lse2;
+    b.delta[stat] = delta;
+  }
   f32x16_t dq[D / 32];
 #pragma unroll
   for (int mb = 0; mb < D / 32; ++mb) dq[mb] = f32x16_t{};
   const float c = a.scale * kLog2e;
-  Stage<D, kBN> sk, sv;
-  if (kt.n > 0) {
-    sk.load(kb, (uint32_t)a.k.token, kt.at(0), t.Lk - 1, tid);
-    sv.load(vb, (uint32_t)a.v.token, kt.at(0), t.Lk - 1, tid);
-    sk.store(lds, tid);
-    sv.store(lds + 2 * kTileB, tid);
-  }
-  __syncthreads();
-  for (int it = 0; it < kt.n; ++it) {
+  Fetch<D, kBN> fetch;
+  fetch.init(lane, wave);
+  const LaneOff lo = lane_off<D>(lane);
+  const long long ks = 2 * a.k.token, vs = 2 * a.v.token;
+  auto step = [&](int it, const char* __restrict__ K, const char* __restrict__ V, char* __restrict__ nextK,
+                  char* __restrict__ nextV) {
     const int j0 = kt.at(it);
-    const char* K = lds + (it & 1) * kTileB;
-    const char* V = lds + (2 + (it & 1)) * kTileB;
-    const bool more = it + 1 < kt.n;
-    if (more) {
-      sk.load(kb, (uint32_t)a.k.token, kt.at(it + 1), t.Lk - 1, tid);
-      sv.load(vb, (uint32_t)a.v.token, kt.at(it + 1), t.Lk - 1, tid);
+    if (it + 1 < kt.n) {
+      fetch(nextK, kb, ks, kt.at(it + 1), t.Lk - 1, wave);
+      fetch(nextV, vb, vs, kt.at(it + 1), t.Lk - 1, wave);
     }
     if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
       const bool all = sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1);
@@ -343,8 +364,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long lon
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
         for (int st = 0; st < D / 16; ++st) {
-          s = mfma32x32x16(row_frag<D>(K, 32 * blk + n, st, h), q[st], s);
-          dp = mfma32x32x16(row_frag<D>(V, 32 * blk + n, st, h), g[st], dp);
+          s = mfma32x32x16(row_frag<D>(K, lo, 32 * blk, st), q[st], s);
+          dp = mfma32x32x16(row_frag<D>(V, lo, 32 * blk, st), g[st], dp);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -356,15 +377,20 @@ __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long lon
           const bf16x8_t df = acc_frag(s, st);
 #pragma unroll
           for (int mb = 0; mb < D / 32; ++mb)
-            dq[mb] = mfma32x32x16(col_frag<D>(K, 32 * blk + 16 * st, mb, lane), df, dq[mb]);
+            dq[mb] = mfma32x32x16(col_frag<D>(K, lo, 32 * blk + 16 * st, mb), df, dq[mb]);
         }
       }
     }
-    if (more) {
-      sk.store(lds + ((it + 1) & 1) * kTileB, tid);
-      sv.store(lds + (2 + ((it + 1) & 1)) * kTileB, tid);
-    }
-    __syncthreads();
+    tiles_ready();
+  };
+  if (kt.n > 0) {
+    fetch(ldsK0, kb, ks, kt.at(0), t.Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(0), t.Lk - 1, wave);
+  }
+  tiles_ready();
+  for (int it = 0; it < kt.n; it += 2) {
+    step(it, ldsK0, ldsV0, ldsK1, ldsV1);
+    if (it + 1 < kt.n) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   if (r0 + n <= last)
     store_rows<D>(b.dq.p + (long long)(t.q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
@@ -374,11 +400,15 @@ __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long lon
 // of every query head that reads it.  S and dP are computed with the queries down, so that P and
 // dS are the right operands of dV^T = dO^T P and dK^T = Q^T dS.
 template <int D>
-__global__ __launch_bounds__(256, 1) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+__global__ __launch_bounds__(256, 2) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
   constexpr int kTileB = kBQ * Tile<D>::kRow;
+  __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
+  __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
+  // the workgroup's V: in registers beside K for D = 64; for D = 128 those and the sums leave no room
+  // for two waves per SIMD, so it stays in LDS
+  constexpr bool kVLds = D == 128;
+  __shared__ __attribute__((aligned(16))) char ldsV[kVLds ? kAttnK * Tile<D>::kRow : 16];
   const AttnArgs& a = b.f;
-  float* stats = reinterpret_cast<float*>(lds + 4 * kTileB);  // [2][2][kBQ]: lse in base 2, row sums
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const int group = a.Hq / a.Hkv;
@@ -393,14 +423,19 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_k(AttnBackwardArgs b, long lo
   const int k0 = (int)kt0, Lq = qr.n, Lk = kr.n;
   const Mask m{Lk - Lq, a.window, a.sinks};
   const int jw = k0 + 32 * wave, j = jw + n, jr = min(j, Lk - 1);  // wave's first key, lane's key
-  bf16x8_t kf[D / 16], vf[D / 16];
+  bf16x8_t kf[D / 16], vf[kVLds ? 1 : D / 16];
   {
     const uint16_t* kp = a.k.p + (long long)(kr.lo + jr) * a.k.token + hk * a.k.head + 8 * h;
-    const uint16_t* vp = a.v.p + (long long)(kr.lo + jr) * a.v.token + hk * a.v.head + 8 * h;
 #pragma unroll
-    for (int st = 0; st < D / 16; ++st) {
-      kf[st] = as_bf16x8(ld16(kp + 16 * st));
-      vf[st] = as_bf16x8(ld16(vp + 16 * st));
+    for (int st = 0; st < D / 16; ++st) kf[st] = as_bf16x8(ld16(kp + 16 * st));
+    if constexpr (kVLds) {
+      Fetch<D, kAttnK> whole;
+      whole.init(lane, wave);
+      whole(ldsV, a.v.p + (long long)kr.lo * a.v.token + hk * a.v.head, 2 * a.v.token, k0, Lk - 1, wave);
+    } else {
+      const uint16_t* vp = a.v.p + (long long)(kr.lo + jr) * a.v.token + hk * a.v.head + 8 * h;
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) vf[st] = as_bf16x8(ld16(vp + 16 * st));
     }
   }
   // queries that see any of the workgroup's keys: [i_lo, i_hi)
@@ -415,42 +450,34 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_k(AttnBackwardArgs b, long lo
 #pragma unroll
   for (int mb = 0; mb < D / 32; ++mb) dk[mb] = dv[mb] = f32x16_t{};
   const float c = a.scale * kLog2e;
-  Stage<D, kBQ> s_q, s_g;
-  float st_v = 0.f;
-  auto load = [&](int it) {
+  Fetch<D, kBQ> fetch;
+  fetch.init(lane, wave);
+  const LaneOff lo = lane_off<D>(lane);
+  const long long qs = 2 * a.q.token, gs = 2 * b.dout.token;
+  const uint16_t* qb = a.q.p + (long long)qr.lo * a.q.token;
+  const uint16_t* gb = b.dout.p + (long long)qr.lo * b.dout.token;
+  auto request = [&](int it, char* __restrict__ Q, char* __restrict__ G, float* __restrict__ st) {
     const int hq = hk * group + it / nt, i0 = (t_lo + it % nt) * kBQ;
-    s_q.load(a.q.p + (long long)qr.lo * a.q.token + hq * a.q.head, (uint32_t)a.q.token, i0, Lq - 1, tid);
-    s_g.load(b.dout.p + (long long)qr.lo * b.dout.token + hq * b.dout.head, (uint32_t)b.dout.token, i0, Lq - 1, tid);
-    if (tid < 2 * kBQ) {
-      const size_t at = (size_t)hq * a.Tq + qr.lo + min(i0 + (tid & (kBQ - 1)), Lq - 1);
-      st_v = tid < kBQ ? a.lse[at] * kLog2e : b.delta[at];
+    fetch(Q, qb + hq * a.q.head, qs, i0, Lq - 1, wave);
+    fetch(G, gb + hq * b.dout.head, gs, i0, Lq - 1, wave);
+    if (wave == 0) {
+      const float* src = (lane < kBQ ? b.lse2 : b.delta) + (size_t)hq * a.Tq + qr.lo + min(i0 + (lane & (kBQ - 1)), Lq - 1);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                       (__attribute__((address_space(3))) void*)st, 4, 0, 0);
     }
   };
-  auto store = [&](int buf) {
-    s_q.store(lds + buf * kTileB, tid);
-    s_g.store(lds + (2 + buf) * kTileB, tid);
-    if (tid < 2 * kBQ) stats[buf * 2 * kBQ + tid] = st_v;
-  };
-  if (total > 0) {
-    load(0);
-    store(0);
-  }
-  __syncthreads();
-  for (int it = 0; it < total; ++it) {
-    const int i0 = (t_lo + it % nt) * kBQ, buf = it & 1;
-    const char* Q = lds + buf * kTileB;
-    const char* G = lds + (2 + buf) * kTileB;
-    const float* ls = stats + buf * 2 * kBQ;
-    const bool more = it + 1 < total;
-    if (more) load(it + 1);
+  auto step = [&](int it, const char* __restrict__ Q, const char* __restrict__ G, const float* __restrict__ ls,
+                  char* __restrict__ nextQ, char* __restrict__ nextG, float* __restrict__ next_st) {
+    if (it + 1 < total) request(it + 1, nextQ, nextG, next_st);
+    const int i0 = (t_lo + it % nt) * kBQ;
     const int p_lo = i0 + m.shift, p_hi = min(i0 + kBQ - 1, Lq - 1) + m.shift;
     if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
       const bool all = i0 + kBQ <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
       f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
-        s = mfma32x32x16(row_frag<D>(Q, n, st, h), kf[st], s);
-        dp = mfma32x32x16(row_frag<D>(G, n, st, h), vf[st], dp);
+        s = mfma32x32x16(row_frag<D>(Q, lo, 0, st), kf[st], s);
+        dp = mfma32x32x16(row_frag<D>(G, lo, 0, st), kVLds ? row_frag<D>(ldsV, lo, 32 * wave, st) : vf[kVLds ? 0 : st], dp);
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -470,13 +497,18 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_k(AttnBackwardArgs b, long lo
         const bf16x8_t pf = acc_frag(s, st), df = acc_frag(dp, st);
 #pragma unroll
         for (int mb = 0; mb < D / 32; ++mb) {
-          dv[mb] = mfma32x32x16(col_frag<D>(G, 16 * st, mb, lane), pf, dv[mb]);
-          dk[mb] = mfma32x32x16(col_frag<D>(Q, 16 * st, mb, lane), df, dk[mb]);
+          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pf, dv[mb]);
+          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), df, dk[mb]);
         }
       }
     }
-    if (more) store(buf ^ 1);
-    __syncthreads();
+    tiles_ready();
+  };
+  if (total > 0) request(0, ldsQ0, ldsG0, st0);
+  tiles_ready();
+  for (int it = 0; it < total; it += 2) {
+    step(it, ldsQ0, ldsG0, st0, ldsQ1, ldsG1, st1);
+    if (it + 1 < total) step(it + 1, ldsQ1, ldsG1, st1, ldsQ0, ldsG0, st0);
   }
   if (j >= Lk) return;
   store_rows<D>(b.dk.p + (long long)(kr.lo + j) * b.dk.token + hk * b.dk.head, dk, a.scale, h);
@@ -488,7 +520,7 @@ namespace {
 template <int D>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
   const long long slots = attn_slots(a.Tq, a.n_seq, kAttnQ);
-  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 4 * kBN * Tile<D>::kRow, s, a, slots);
+  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 0, s, a, slots);
   return hipGetLastError();
 }
 
@@ -497,12 +529,11 @@ hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
   const AttnArgs& a = b.f;
   const long long qs = attn_slots(a.Tq, a.n_seq, kAttnQ), ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
   if (a.Tq > 0) {
-    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 4 * kBN * Tile<D>::kRow, s, b, qs);
+    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 0, s, b, qs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)(ks * a.Hkv)), dim3(256),
-                     4 * kBQ * Tile<D>::kRow + 4 * kBQ * sizeof(float), s, b, ks);
+  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)(ks * a.Hkv)), dim3(256), 0, s, b, ks);
   return hipGetLastError();
 }
 

@@ -237,7 +237,8 @@ int molora_attn_backward(const molora_attn_shape* shape, const molora_rows* dout
   b.dq = rows_of(dq);
   b.dk = rows_of(dk);
   b.dv = rows_of(dv);
-  b.delta = static_cast<float*>(ws);
+  b.lse2 = static_cast<float*>(ws);
+  b.delta = b.lse2 + molora::attn_stat_bytes(shape->Tq, Hq) / sizeof(float);
   const hipError_t e = molora::launch_attn_backward(b, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attn_backward launch");
 }

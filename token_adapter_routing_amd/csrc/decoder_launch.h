@@ -41,7 +41,8 @@ hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t s);
 struct AttnBackwardArgs {
   AttnArgs f;  // o and lse as the forward wrote them
   Rows dout, dq, dk, dv;
-  float* delta;  // workspace [Hq][Tq]
+  float* lse2;   // workspace [Hq][Tq]: lse in base 2
+  float* delta;  // workspace [Hq][Tq]: rowsum(dO O)
 };
 hipError_t launch_attn_backward(const AttnBackwardArgs& a, hipStream_t s);
 

@@ -18,8 +18,9 @@ constexpr int kAttnK = 128;   // key rows per workgroup of the dk / dv pass
 MOLORA_HD inline long long attn_slot0(int off, int s, int tile) { return (long long)(off / tile) + s; }
 MOLORA_HD inline long long attn_slots(int T, int n_seq, int tile) { return (long long)(T / tile) + n_seq; }
 
-// backward: rowsum(dO O), fp32 [heads][Tq]
-inline size_t attn_backward_ws_bytes(int Tq, int heads) { return align256((size_t)Tq * heads * sizeof(float)); }
+// backward: lse in base 2 and rowsum(dO O), fp32 [heads][Tq] each
+inline size_t attn_stat_bytes(int Tq, int heads) { return align256((size_t)Tq * heads * sizeof(float)); }
+inline size_t attn_backward_ws_bytes(int Tq, int heads) { return 2 * attn_stat_bytes(Tq, heads); }
 
 // ---- decode attention: blocks of kDecBlock positions; a sequence's visible blocks are split
 // evenly over `splits` workgroups, at least kDecMinBlocks each.  Partial results per (sequence,
