@@ -25,7 +25,7 @@ namespace molora {
 namespace {
 
 constexpr int kBN = 64;  // keys per LDS tile of the forward and the dq pass
-constexpr int kBQ = 32;  // queries per LDS tile of the dk / dv pass
+constexpr int kBQ = kAttnStep;  // queries per LDS tile of the dk / dv pass
 
 template <int D>
 struct Tile {
@@ -125,13 +125,33 @@ struct QTile {
   int row0, Lq, Lk, q0, k0;
   bool ok;
 };
-__device__ __forceinline__ QTile find_q_tile(const AttnArgs& a, long long slot) {
+// A slot's query tile.  With up to 64 sequences the longest sequence comes first and in it the last
+// tile, which sees the most keys: workgroups start in this order, so the long ones do not come last,
+// and those of one sequence, which read the same keys, run together.  With more sequences the slots
+// run through them from the end.
+__device__ __forceinline__ QTile find_q_tile(const AttnArgs& a, long long slot, long long slots) {
   QTile t{};
-  const int s = __builtin_amdgcn_readfirstlane(
-      wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.q_off[i], 0), a.Tq), i, kAttnQ); }));
-  if (s < 0) return t;
+  int s;
+  long long row0;
+  if (a.n_seq <= kWave) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    if (lane < a.n_seq) {
+      const int q0 = min(max(a.q_off[lane], 0), a.Tq), q1 = min(max(a.q_off[lane + 1], 0), a.Tq);
+      n = (max(q1 - q0, 0) + kAttnQ - 1) / kAttnQ;
+    }
+    int tile = 0;
+    s = ranked_tile(n, a.n_seq, slot, &tile);
+    if (s < 0) return t;
+    row0 = (long long)(__builtin_amdgcn_readlane(n, s) - 1 - tile) * kAttnQ;
+  } else {
+    slot = slots - 1 - slot;
+    s = __builtin_amdgcn_readfirstlane(
+        wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.q_off[i], 0), a.Tq), i, kAttnQ); }));
+    if (s < 0) return t;
+    row0 = (slot - attn_slot0(min(max(a.q_off[s], 0), a.Tq), s, kAttnQ)) * kAttnQ;
+  }
   const SeqRange q = seq_range(a.q_off, s, a.Tq), k = seq_range(a.kv_off, s, a.Tkv);
-  const long long row0 = (slot - attn_slot0(q.lo, s, kAttnQ)) * kAttnQ;
   t.row0 = (int)row0;
   t.Lq = q.n;
   t.Lk = k.n;
@@ -166,17 +186,17 @@ __device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int 
 }
 
 // Workgroup -> (head, slot): the heads of one key-value head follow each other on one XCD
-// (consecutive workgroups go round the XCDs), the longest tiles of a sequence come first.
+// (consecutive workgroups go round the XCDs).
 struct Place {
   int hq, hk;
   long long slot;
 };
-__device__ __forceinline__ Place place(const AttnArgs& a, long long slots) {
+__device__ __forceinline__ Place place(const AttnArgs& a) {
   const int g = a.Hq / a.Hkv;
   const long long id = blockIdx.x;
   const int hk = (int)(id % a.Hkv);
   const long long rest = id / a.Hkv;
-  return {hk * g + (int)(rest % g), hk, slots - 1 - rest / g};
+  return {hk * g + (int)(rest % g), hk, rest / g};
 }
 
 // Stores a 32 x D block held as D x 32 (column = row of the output), times `mul`.
@@ -202,8 +222,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a, slots);
-  const QTile t = find_q_tile(a, pl.slot);
+  const Place pl = place(a);
+  const QTile t = find_q_tile(a, pl.slot, slots);
   if (!t.ok) return;
   const Mask m{t.Lk - t.Lq, a.window, a.sinks};
   const int last = t.Lq - 1;
@@ -300,14 +320,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
 // the keys as the forward does.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long long slots) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, long long slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a, slots);
-  const QTile t = find_q_tile(a, pl.slot);
+  const Place pl = place(a);
+  const QTile t = find_q_tile(a, pl.slot, slots);
   if (!t.ok) return;
   const Mask m{t.Lk - t.Lq, a.window, a.sinks};
   const int last = t.Lq - 1;
@@ -396,68 +416,126 @@ __global__ __launch_bounds__(256, 2) void attn_dq_k(AttnBackwardArgs b, long lon
     store_rows<D>(b.dq.p + (long long)(t.q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
 }
 
+namespace {
+
+// A key tile of the dk / dv pass: 128 keys of one key-value head, the queries that see any of them
+// in steps of kBQ rows, taken for every query head that reads the head: `total` steps in `chunks`
+// workgroups of `per` steps.  per comes from the longest tile's steps, so that chunks are about
+// equally long and short tiles are not split.
+struct KvTile {
+  SeqRange q, k;
+  int k0, t_lo, nt, total, chunks, per;
+  long long part;  // of chunk 0
+  bool ok;
+};
+
+// The tile of place `slot`, or with `sink` set of sinks' tile `slot`.
+__device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool sink, long long slot) {
+  const AttnArgs& a = b.f;
+  KvTile t{};
+  int s;
+  long long k0;
+  if (sink) {
+    s = (int)(slot / b.sink_tiles);
+    k0 = slot % b.sink_tiles * kAttnK;
+  } else if (a.n_seq <= kWave) {  // the longest sequence first, in it the first keys, which the most queries see
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    if (lane < a.n_seq) {
+      const int k0 = min(max(a.kv_off[lane], 0), a.Tkv), k1 = min(max(a.kv_off[lane + 1], 0), a.Tkv);
+      n = (max(k1 - k0, 0) + kAttnK - 1) / kAttnK;
+    }
+    int tile = 0;
+    s = ranked_tile(n, a.n_seq, slot, &tile);
+    if (s < 0) return t;
+    k0 = (long long)tile * kAttnK;
+  } else {
+    s = __builtin_amdgcn_readfirstlane(
+        wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.kv_off[i], 0), a.Tkv), i, kAttnK); }));
+    if (s < 0) return t;
+    k0 = (slot - attn_slot0(min(max(a.kv_off[s], 0), a.Tkv), s, kAttnK)) * kAttnK;
+  }
+  t.q = seq_range(a.q_off, s, a.Tq);
+  t.k = seq_range(a.kv_off, s, a.Tkv);
+  if (k0 < 0 || k0 >= t.k.n || (!sink && k0 < (long long)b.sink_tiles * kAttnK)) return t;
+  t.ok = true;
+  t.k0 = (int)k0;
+  const int shift = t.k.n - t.q.n, group = a.Hq / a.Hkv;
+  const int i_lo = max(t.k0 - shift, 0);
+  int i_hi = t.q.n;
+  if (a.window && t.k0 >= a.sinks) {
+    const long long end = (long long)min(t.k0 + kAttnK, t.k.n) - 1 + a.window - shift;
+    i_hi = (int)max(0ll, min((long long)t.q.n, end));
+  }
+  t.t_lo = i_lo / kBQ;
+  t.nt = max((i_hi + kBQ - 1) / kBQ - t.t_lo, 0);
+  t.total = t.nt * group;
+  const int steps = (t.q.n + kBQ - 1) / kBQ * group, splits = sink ? b.sink_splits : b.splits;
+  t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, kAttnMinSteps);
+  t.chunks = max((t.total + t.per - 1) / t.per, 1);
+  const long long sink_parts = (long long)b.sink_tiles * a.n_seq * b.sink_splits;
+  t.part = sink ? slot * splits : sink_parts + slot * splits;
+  return t;
+}
+
+}  // namespace
+
 // dK and dV: a workgroup holds 128 keys of one key-value head, 32 per wave, and walks the queries
-// of every query head that reads it.  S and dP are computed with the queries down, so that P and
-// dS are the right operands of dV^T = dO^T P and dK^T = Q^T dS.
+// of every query head that reads it (or one chunk of them, whose sums go to the workspace).  S and
+// dP are computed with the queries down, so that P and dS are the right operands of dV^T = dO^T P
+// and dK^T = Q^T dS.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
   constexpr int kTileB = kBQ * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
   __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
-  // the workgroup's V: in registers beside K for D = 64; for D = 128 those and the sums leave no room
-  // for two waves per SIMD, so it stays in LDS
-  constexpr bool kVLds = D == 128;
-  __shared__ __attribute__((aligned(16))) char ldsV[kVLds ? kAttnK * Tile<D>::kRow : 16];
+  // The workgroup's V stays in LDS: beside K's operands and the sums of dK and dV in registers it would
+  // cost a wave per SIMD (4 x 4096 tokens, 16 heads of 64: 451 us with V in registers and two waves,
+  // 402 us with three; heads of 128: two waves instead of one, 1438 -> 794 us).
+  __shared__ __attribute__((aligned(16))) char ldsV[kAttnK * Tile<D>::kRow];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const int group = a.Hq / a.Hkv;
+  // The sinks' tiles come first.  The chunk is the slowest index: workgroups without work then lie
+  // together at the end (spread between the others they would leave whole CUs idle).
   const int hk = (int)(blockIdx.x % a.Hkv);
-  const long long slot = blockIdx.x / a.Hkv;  // the first keys are seen by the most queries
-  const int sq = __builtin_amdgcn_readfirstlane(
-      wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.kv_off[i], 0), a.Tkv), i, kAttnK); }));
-  if (sq < 0) return;
-  const SeqRange qr = seq_range(a.q_off, sq, a.Tq), kr = seq_range(a.kv_off, sq, a.Tkv);
-  const long long kt0 = (slot - attn_slot0(kr.lo, sq, kAttnK)) * kAttnK;
-  if (kt0 < 0 || kt0 >= kr.n) return;
-  const int k0 = (int)kt0, Lq = qr.n, Lk = kr.n;
+  long long id = blockIdx.x / a.Hkv;
+  const long long sinks = (long long)b.sink_tiles * a.n_seq, first = sinks * b.sink_splits;
+  const bool sink = id < first;
+  if (!sink) id -= first;
+  const long long n_tiles = sink ? sinks : slots;
+  const int chunk = (int)(id / n_tiles);
+  const KvTile t = find_kv_tile(b, sink, id % n_tiles);
+  if (!t.ok || chunk >= t.chunks) return;
+  const SeqRange qr = t.q, kr = t.k;
+  const int k0 = t.k0, Lq = qr.n, Lk = kr.n, nt = t.nt;
+  const int it0 = chunk * t.per, it1 = min(it0 + t.per, t.total);
   const Mask m{Lk - Lq, a.window, a.sinks};
   const int jw = k0 + 32 * wave, j = jw + n, jr = min(j, Lk - 1);  // wave's first key, lane's key
-  bf16x8_t kf[D / 16], vf[kVLds ? 1 : D / 16];
+  bf16x8_t kf[D / 16];
   {
     const uint16_t* kp = a.k.p + (long long)(kr.lo + jr) * a.k.token + hk * a.k.head + 8 * h;
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) kf[st] = as_bf16x8(ld16(kp + 16 * st));
-    if constexpr (kVLds) {
-      Fetch<D, kAttnK> whole;
-      whole.init(lane, wave);
-      whole(ldsV, a.v.p + (long long)kr.lo * a.v.token + hk * a.v.head, 2 * a.v.token, k0, Lk - 1, wave);
-    } else {
-      const uint16_t* vp = a.v.p + (long long)(kr.lo + jr) * a.v.token + hk * a.v.head + 8 * h;
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st) vf[st] = as_bf16x8(ld16(vp + 16 * st));
-    }
+    Fetch<D, kAttnK> whole;
+    whole.init(lane, wave);
+    whole(ldsV, a.v.p + (long long)kr.lo * a.v.token + hk * a.v.head, 2 * a.v.token, k0, Lk - 1, wave);
   }
-  // queries that see any of the workgroup's keys: [i_lo, i_hi)
-  const int i_lo = max(k0 - m.shift, 0);
-  int i_hi = Lq;
-  if (m.window && k0 >= m.sinks) {
-    const long long end = (long long)min(k0 + kAttnK, Lk) - 1 + m.window - m.shift;
-    i_hi = (int)max(0ll, min((long long)Lq, end));
-  }
-  const int t_lo = i_lo / kBQ, nt = max((i_hi + kBQ - 1) / kBQ - t_lo, 0), total = nt * group;
   f32x16_t dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int mb = 0; mb < D / 32; ++mb) dk[mb] = dv[mb] = f32x16_t{};
   const float c = a.scale * kLog2e;
   Fetch<D, kBQ> fetch;
   fetch.init(lane, wave);
-  const LaneOff lo = lane_off<D>(lane);
+  const LaneOff lo0 = lane_off<D>(lane);
   const long long qs = 2 * a.q.token, gs = 2 * b.dout.token;
   const uint16_t* qb = a.q.p + (long long)qr.lo * a.q.token;
   const uint16_t* gb = b.dout.p + (long long)qr.lo * b.dout.token;
+  // The queries from the last on: every key tile of a causal sequence ends there, so the workgroups
+  // that run together read the same rows.
   auto request = [&](int it, char* __restrict__ Q, char* __restrict__ G, float* __restrict__ st) {
-    const int hq = hk * group + it / nt, i0 = (t_lo + it % nt) * kBQ;
+    const int hq = hk * group + it / nt, i0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
     fetch(Q, qb + hq * a.q.head, qs, i0, Lq - 1, wave);
     fetch(G, gb + hq * b.dout.head, gs, i0, Lq - 1, wave);
     if (wave == 0) {
@@ -468,8 +546,11 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_k(AttnBackwardArgs b, long lo
   };
   auto step = [&](int it, const char* __restrict__ Q, const char* __restrict__ G, const float* __restrict__ ls,
                   char* __restrict__ nextQ, char* __restrict__ nextG, float* __restrict__ next_st) {
-    if (it + 1 < total) request(it + 1, nextQ, nextG, next_st);
-    const int i0 = (t_lo + it % nt) * kBQ;
+    if (it + 1 < it1) request(it + 1, nextQ, nextG, next_st);
+    const int i0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
+    LaneOff lo = lo0;
+    // opaque: the operands' addresses are made when needed; kept in registers they would spill others
+    asm volatile("" : "+v"(lo.row), "+v"(lo.col));
     const int p_lo = i0 + m.shift, p_hi = min(i0 + kBQ - 1, Lq - 1) + m.shift;
     if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
       const bool all = i0 + kBQ <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
@@ -477,7 +558,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_k(AttnBackwardArgs b, long lo
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
         s = mfma32x32x16(row_frag<D>(Q, lo, 0, st), kf[st], s);
-        dp = mfma32x32x16(row_frag<D>(G, lo, 0, st), kVLds ? row_frag<D>(ldsV, lo, 32 * wave, st) : vf[kVLds ? 0 : st], dp);
+        dp = mfma32x32x16(row_frag<D>(G, lo, 0, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -504,15 +585,62 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_k(AttnBackwardArgs b, long lo
     }
     tiles_ready();
   };
-  if (total > 0) request(0, ldsQ0, ldsG0, st0);
+  if (it0 < it1) request(it0, ldsQ0, ldsG0, st0);
   tiles_ready();
-  for (int it = 0; it < total; it += 2) {
+  for (int it = it0; it < it1; it += 2) {
     step(it, ldsQ0, ldsG0, st0, ldsQ1, ldsG1, st1);
-    if (it + 1 < total) step(it + 1, ldsQ1, ldsG1, st1, ldsQ0, ldsG0, st0);
+    if (it + 1 < it1) step(it + 1, ldsQ1, ldsG1, st1, ldsQ0, ldsG0, st0);
+  }
+  if (t.chunks > 1) {
+    // fp32 sums [2][128][D] of this chunk
+    float* part = b.part + ((size_t)(t.part + chunk) * a.Hkv + hk) * attn_part_floats(D);
+#pragma unroll
+    for (int mb = 0; mb < D / 32; ++mb)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float* at = part + (size_t)(32 * wave + n) * D + 32 * mb + 8 * g + 4 * h;
+        f32x4_t x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = dk[mb][4 * g + i];
+          y[i] = dv[mb][4 * g + i];
+        }
+        *reinterpret_cast<f32x4_t*>(at) = x;
+        *reinterpret_cast<f32x4_t*>(at + (size_t)kAttnK * D) = y;
+      }
+    return;
   }
   if (j >= Lk) return;
   store_rows<D>(b.dk.p + (long long)(kr.lo + j) * b.dk.token + hk * b.dk.head, dk, a.scale, h);
   store_rows<D>(b.dv.p + (long long)(kr.lo + j) * b.dv.token + hk * b.dv.head, dv, 1.f, h);
+}
+
+// Adds the chunks of the key tiles that were split, in order: kJoinParts workgroups per tile.
+constexpr int kJoinParts = 16;
+template <int D>
+__global__ __launch_bounds__(256) void attn_dkv_join_k(AttnBackwardArgs b) {
+  const AttnArgs& a = b.f;
+  const int hk = (int)(blockIdx.x % a.Hkv), piece = (int)(blockIdx.x / a.Hkv % kJoinParts);
+  const long long id = blockIdx.x / a.Hkv / kJoinParts, sinks = (long long)b.sink_tiles * a.n_seq;
+  const KvTile t = find_kv_tile(b, id < sinks, id < sinks ? id : id - sinks);
+  if (!t.ok || t.chunks == 1) return;
+  const float* part = b.part + ((size_t)t.part * a.Hkv + hk) * attn_part_floats(D);
+  const size_t next = (size_t)a.Hkv * attn_part_floats(D);
+  constexpr int kQuads = D / 4, kRows = kAttnK / kJoinParts;
+  for (int i = threadIdx.x; i < 2 * kRows * kQuads; i += 256) {
+    const int which = i / (kRows * kQuads), row = kRows * piece + i / kQuads % kRows, c = i % kQuads * 4;
+    if (t.k0 + row >= t.k.n) continue;
+    const float* at = part + (size_t)which * kAttnK * D + (size_t)row * D + c;
+    f32x4_t x = *reinterpret_cast<const f32x4_t*>(at);
+#pragma unroll 4
+    for (int ch = 1; ch < t.chunks; ++ch) x += *reinterpret_cast<const f32x4_t*>(at + ch * next);
+    const Rows& o = which ? b.dv : b.dk;
+    const float mul = which ? 1.f : a.scale;
+    uint2 v;
+    v.x = pack_bf16x2(x[0] * mul, x[1] * mul);
+    v.y = pack_bf16x2(x[2] * mul, x[3] * mul);
+    *reinterpret_cast<uint2*>(o.p + (long long)(t.k.lo + t.k0 + row) * o.token + hk * o.head + c) = v;
+  }
 }
 
 namespace {
@@ -533,7 +661,13 @@ hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)(ks * a.Hkv)), dim3(256), 0, s, b, ks);
+  const long long sinks = (long long)b.sink_tiles * a.n_seq;
+  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,
+                     ks);
+  const hipError_t e = hipGetLastError();
+  const long long joins = sinks + (b.splits > 1 ? ks : 0);
+  if (e != hipSuccess || joins == 0) return e;
+  hipLaunchKernelGGL((attn_dkv_join_k<D>), dim3((unsigned)(joins * a.Hkv * kJoinParts)), dim3(256), 0, s, b);
   return hipGetLastError();
 }
 

@@ -80,7 +80,7 @@ int check_shape(const molora_attn_shape* s) {
   if (s->n_seq >= kMaxRows || s->Tq >= kMaxRows || s->Tkv >= kMaxRows)
     return fail(MOLORA_ENOTSUP, "n_seq=%d, Tq=%d, Tkv=%d too large", s->n_seq, s->Tq, s->Tkv);
   if (std::max(molora::attn_slots(s->Tq, s->n_seq, molora::kAttnQ) * s->n_heads,
-               molora::attn_slots(s->Tkv, s->n_seq, molora::kAttnK) * s->n_kv_heads) >= (1ll << 31))
+               molora::attn_slots(s->Tkv, s->n_seq, molora::kAttnK) * s->n_kv_heads * 32) >= (1ll << 31))
     return fail(MOLORA_ENOTSUP, "too many (tile, head) pairs");
   if ((rc = check_mask(s->window, s->sinks, s->scale)) != MOLORA_OK) return rc;
   if (s->n_seq > 0 && (s->q_off == nullptr || !aligned(s->q_off, 4) || !aligned(s->kv_off, 4)))
@@ -107,6 +107,11 @@ molora::AttnArgs attn_args(const molora_attn_shape* s, const molora_rows* q, con
   a.sinks = s->sinks;
   a.scale = s->scale;
   return a;
+}
+
+molora::AttnBwdPlan bwd_plan_of(const molora_attn_shape* s) {
+  return molora::attn_bwd_plan(s->Tq, s->Tkv, s->n_seq, s->n_heads, s->n_kv_heads, s->head_dim, s->window,
+                               s->sinks);
 }
 
 int check_cache(const molora_kv_cache* c) {
@@ -206,7 +211,7 @@ int molora_attn_backward_workspace(const molora_attn_shape* shape, size_t* bytes
   if (bytes == nullptr) return fail(MOLORA_EINVAL, "bytes is NULL");
   const int rc = check_shape(shape);
   if (rc != MOLORA_OK) return rc;
-  *bytes = molora::attn_backward_ws_bytes(shape->Tq, shape->n_heads);
+  *bytes = bwd_plan_of(shape).total;
   return ok();
 }
 
@@ -227,9 +232,9 @@ int molora_attn_backward(const molora_attn_shape* shape, const molora_rows* dout
   if ((rc = check_rows(dv, "dv", shape->Tkv, Hkv, D, true)) != MOLORA_OK) return rc;
   if (shape->n_seq == 0 || (shape->Tq == 0 && shape->Tkv == 0)) return ok();
   if (shape->Tq > 0 && (lse == nullptr || !aligned(lse, 4))) return fail(MOLORA_EINVAL, "lse NULL or misaligned");
-  const size_t need = molora::attn_backward_ws_bytes(shape->Tq, Hq);
-  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
-    return fail(MOLORA_ENOSPC, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need, ws_bytes);
+  const molora::AttnBwdPlan plan = bwd_plan_of(shape);
+  if (plan.total > 0 && (ws == nullptr || ws_bytes < plan.total || !aligned(ws, 256)))
+    return fail(MOLORA_ENOSPC, "workspace of %zu bytes (256-byte aligned) needed, %zu given", plan.total, ws_bytes);
   molora::AttnBackwardArgs b{};
   b.f = attn_args(shape, q, k, v, o);
   b.f.lse = const_cast<float*>(lse);
@@ -237,8 +242,14 @@ int molora_attn_backward(const molora_attn_shape* shape, const molora_rows* dout
   b.dq = rows_of(dq);
   b.dk = rows_of(dk);
   b.dv = rows_of(dv);
-  b.lse2 = static_cast<float*>(ws);
-  b.delta = b.lse2 + molora::attn_stat_bytes(shape->Tq, Hq) / sizeof(float);
+  char* base = static_cast<char*>(ws);
+  b.lse2 = reinterpret_cast<float*>(base + plan.lse_off);
+  b.delta = reinterpret_cast<float*>(base + plan.delta_off);
+  b.part = reinterpret_cast<float*>(base + plan.part_off);
+  b.splits = plan.splits;
+  b.sink_splits = plan.sink_splits;
+  b.sink_tiles = plan.sink_tiles;
+  b.most = plan.most;
   const hipError_t e = molora::launch_attn_backward(b, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attn_backward launch");
 }

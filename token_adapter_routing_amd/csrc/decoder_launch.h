@@ -43,6 +43,8 @@ struct AttnBackwardArgs {
   Rows dout, dq, dk, dv;
   float* lse2;   // workspace [Hq][Tq]: lse in base 2
   float* delta;  // workspace [Hq][Tq]: rowsum(dO O)
+  int splits, sink_splits, sink_tiles, most;  // attn_bwd_plan
+  float* part;   // workspace: the split key tiles' sums
 };
 hipError_t launch_attn_backward(const AttnBackwardArgs& a, hipStream_t s);
 

@@ -22,6 +22,47 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
   return p;
 }
 
+// A causal sequence's key tiles are seen by unequal numbers of queries, so with few tiles the longest
+// one sets the time: chunks until there are kBwdTarget workgroups, two for each of the 512 places
+// that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 2127 us unsplit, 1525 us
+// in 4 chunks).  With a window a tile sees a window's worth, but the sinks' tiles every query: those
+// are taken apart, in up to 16 chunks (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: 2300 us
+// unsplit, 373 us in 15 chunks).
+AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks) {
+  constexpr long long kBwdTarget = 1024, kBwdPartBytes = 512ll << 20;
+  AttnBwdPlan p{};
+  const long long slots = attn_slots(Tkv, n_seq, kAttnK), units = slots * n_kv_heads, group = n_heads / n_kv_heads;
+  const long long steps = ((long long)Tq + kAttnStep - 1) / kAttnStep * group;
+  const long long bytes = (long long)(attn_part_floats(head_dim) * sizeof(float));
+  const bool windowed = window > 0 && window < Tq;
+  p.most = (int)std::min(steps, windowed ? ((long long)window + kAttnK + 2 * kAttnStep - 2) / kAttnStep * group : steps);
+  p.splits = p.sink_splits = 1;
+  if (units > 0) {
+    p.splits = (int)std::max(1ll, std::min({(kBwdTarget + units - 1) / units, 16ll,
+                                            ((long long)p.most + kAttnMinSteps - 1) / kAttnMinSteps,
+                                            kBwdPartBytes / (units * bytes)}));
+    if (windowed && sinks > 0) {
+      const long long per_seq = (std::min((long long)sinks, (long long)Tkv) + kAttnK - 1) / kAttnK;
+      const long long tiles = per_seq * n_seq;
+      const long long n = std::min({2 * kBwdTarget / (tiles * n_kv_heads), 16ll,
+                                    (steps + kAttnMinSteps - 1) / kAttnMinSteps,
+                                    kBwdPartBytes / (tiles * n_kv_heads * bytes)});
+      if (tiles > 0 && n > 1) {
+        p.sink_splits = (int)n;
+        p.sink_tiles = (int)per_seq;
+      }
+    }
+  }
+  const size_t stat = align256((size_t)Tq * n_heads * sizeof(float));
+  const long long parts = (p.sink_tiles > 0 ? (long long)p.sink_tiles * n_seq * p.sink_splits : 0) +
+                          (p.splits > 1 ? slots * p.splits : 0);
+  p.lse_off = 0;
+  p.delta_off = stat;
+  p.part_off = 2 * stat;
+  p.total = p.part_off + (size_t)(parts * n_kv_heads * bytes);
+  return p;
+}
+
 XfServePlan xf_serve_plan(int N, int d, int f, size_t lora_bytes, size_t part_bytes) {
   XfServePlan p{};
   const size_t nd = align256((size_t)N * d * sizeof(uint16_t)), nf = align256((size_t)N * f * sizeof(uint16_t));

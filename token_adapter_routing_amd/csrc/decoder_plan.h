@@ -18,9 +18,18 @@ constexpr int kAttnK = 128;   // key rows per workgroup of the dk / dv pass
 MOLORA_HD inline long long attn_slot0(int off, int s, int tile) { return (long long)(off / tile) + s; }
 MOLORA_HD inline long long attn_slots(int T, int n_seq, int tile) { return (long long)(T / tile) + n_seq; }
 
-// backward: lse in base 2 and rowsum(dO O), fp32 [heads][Tq] each
-inline size_t attn_stat_bytes(int Tq, int heads) { return align256((size_t)Tq * heads * sizeof(float)); }
-inline size_t attn_backward_ws_bytes(int Tq, int heads) { return 2 * attn_stat_bytes(Tq, heads); }
+// Backward: lse in base 2 and rowsum(dO O), fp32 [heads][Tq] each, then the sums of the key tiles that
+// are split into chunks, [2][kAttnK][head_dim] fp32 per (tile, chunk, kv head): first the sinks' tiles
+// (sink_tiles > 0: that many of every sequence, in sink_splits chunks), then the others (splits > 1).
+constexpr int kAttnStep = 32;      // query rows per step of the dk / dv pass
+constexpr int kAttnMinSteps = 32;  // steps per chunk, at least
+struct AttnBwdPlan {
+  int splits, sink_splits, sink_tiles;
+  int most;  // steps of the longest tile that is not a sinks' tile
+  size_t lse_off, delta_off, part_off, total;
+};
+AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks);
+MOLORA_HD inline size_t attn_part_floats(int head_dim) { return (size_t)2 * kAttnK * head_dim; }
 
 // ---- decode attention: blocks of kDecBlock positions; a sequence's visible blocks are split
 // evenly over `splits` workgroups, at least kDecMinBlocks each.  Partial results per (sequence,

@@ -38,6 +38,23 @@ __device__ __forceinline__ int wave_search(int n, long long x, Key key) {
   }
 }
 
+// Tiles of up to 64 sequences, the longest sequence first: lane s holds sequence s's number of tiles
+// (0 past the last).  The sequence of the rank-th tile, -1 past the last, and in *tile its place in
+// the sequence.
+__device__ __forceinline__ int ranked_tile(int n, int n_seq, long long rank, int* tile) {
+  const int lane = threadIdx.x & 63;
+  long long first = 0;  // tiles of the sequences before this one
+  for (int s = 0; s < n_seq; ++s) {
+    const int m = __builtin_amdgcn_readlane(n, s);
+    if (m > n || (m == n && s < lane)) first += m;
+  }
+  const uint64_t mine = __ballot(n > 0 && first <= rank && rank < first + n);
+  if (mine == 0) return -1;
+  const int s = __builtin_ctzll(mine);
+  *tile = __builtin_amdgcn_readlane((int)(rank - first), s);
+  return s;
+}
+
 // Row range of sequence s, limited to [0, T].
 struct SeqRange {
   int lo, n;

@@ -203,9 +203,11 @@ def molora_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     return out, lse
 
 
-def molora_attn_backward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor) -> int:
+def molora_attn_backward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor, window: int = 0,
+                                   sinks: int = 0) -> int:
     n = _c_sz()
-    _check(_library().molora_attn_backward_workspace(ctypes.byref(_shape(q, k, q_off, None, None, 0, 0)), ctypes.byref(n)))
+    _check(_library().molora_attn_backward_workspace(ctypes.byref(_shape(q, k, q_off, None, None, window, sinks)),
+                                                     ctypes.byref(n)))
     return n.value
 
 
