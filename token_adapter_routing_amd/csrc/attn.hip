@@ -110,6 +110,19 @@ __device__ __forceinline__ bf16x8_t col_frag(const char* lds, LaneOff o, int row
   return u.v;
 }
 
+// Schedule of a run of N steps of M products, each step with R operand reads from LDS: the reads of A
+// steps go ahead, so that a product does not wait for the read before it.
+template <int N, int M, int R, int A>
+__device__ __forceinline__ void reads_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, A * R, 0);
+#pragma unroll
+  for (int i = 0; i < N - A; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, A * M, 0);
+}
+
 // Right operand from registers: rows 16 s .. + 15 of a 32x32 result, rounded to bf16.
 __device__ __forceinline__ bf16x8_t acc_frag(const f32x16_t& v, int s) {
   u32x4_t u;
@@ -119,47 +132,6 @@ __device__ __forceinline__ bf16x8_t acc_frag(const f32x16_t& v, int s) {
 }
 
 __device__ __forceinline__ int acc_row(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
-
-// A query tile: sequence, first row, lengths, first rows in the packed tensors.
-struct QTile {
-  int row0, Lq, Lk, q0, k0;
-  bool ok;
-};
-// A slot's query tile.  With up to 64 sequences the longest sequence comes first and in it the last
-// tile, which sees the most keys: workgroups start in this order, so the long ones do not come last,
-// and those of one sequence, which read the same keys, run together.  With more sequences the slots
-// run through them from the end.
-__device__ __forceinline__ QTile find_q_tile(const AttnArgs& a, long long slot, long long slots) {
-  QTile t{};
-  int s;
-  long long row0;
-  if (a.n_seq <= kWave) {
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    if (lane < a.n_seq) {
-      const int q0 = min(max(a.q_off[lane], 0), a.Tq), q1 = min(max(a.q_off[lane + 1], 0), a.Tq);
-      n = (max(q1 - q0, 0) + kAttnQ - 1) / kAttnQ;
-    }
-    int tile = 0;
-    s = ranked_tile(n, a.n_seq, slot, &tile);
-    if (s < 0) return t;
-    row0 = (long long)(__builtin_amdgcn_readlane(n, s) - 1 - tile) * kAttnQ;
-  } else {
-    slot = slots - 1 - slot;
-    s = __builtin_amdgcn_readfirstlane(
-        wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.q_off[i], 0), a.Tq), i, kAttnQ); }));
-    if (s < 0) return t;
-    row0 = (slot - attn_slot0(min(max(a.q_off[s], 0), a.Tq), s, kAttnQ)) * kAttnQ;
-  }
-  const SeqRange q = seq_range(a.q_off, s, a.Tq), k = seq_range(a.kv_off, s, a.Tkv);
-  t.row0 = (int)row0;
-  t.Lq = q.n;
-  t.Lk = k.n;
-  t.q0 = q.lo;
-  t.k0 = k.lo;
-  t.ok = row0 >= 0 && row0 < q.n;
-  return t;
-}
 
 // Key tiles a query tile visits: the sinks' first, then the window's.
 struct KeyTiles {
@@ -188,15 +160,11 @@ __device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int 
 // Workgroup -> (head, slot): the heads of one key-value head follow each other on one XCD
 // (consecutive workgroups go round the XCDs).
 struct Place {
-  int hq, hk;
-  long long slot;
+  int hq, hk, slot;
 };
 __device__ __forceinline__ Place place(const AttnArgs& a) {
-  const int g = a.Hq / a.Hkv;
-  const long long id = blockIdx.x;
-  const int hk = (int)(id % a.Hkv);
-  const long long rest = id / a.Hkv;
-  return {hk * g + (int)(rest % g), hk, rest / g};
+  const unsigned g = a.Hq / a.Hkv, id = blockIdx.x, rest = id / a.Hkv, hk = id % a.Hkv;
+  return {(int)(hk * g + rest % g), (int)hk, (int)(rest / g)};
 }
 
 // Stores a 32 x D block held as D x 32 (column = row of the output), times `mul`.
@@ -217,24 +185,25 @@ __device__ __forceinline__ void store_rows(uint16_t* row, const f32x16_t* acc, f
 
 // A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.
 template <int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots) {
+__global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const Place pl = place(a);
-  const QTile t = find_q_tile(a, pl.slot, slots);
+  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
   if (!t.ok) return;
-  const Mask m{t.Lk - t.Lq, a.window, a.sinks};
-  const int last = t.Lq - 1;
-  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.Lk);
+  const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
+  const Mask m{Lk - Lq, a.window, a.sinks};
+  const int last = Lq - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
-  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + pl.hk * a.k.head;
-  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + pl.hk * a.v.head;
+  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + pl.hk * a.v.head;
   bf16x8_t q[D / 16];
   {
-    const uint16_t* qr = a.q.p + (long long)(t.q0 + r) * a.q.token + pl.hq * a.q.head + 8 * h;
+    const uint16_t* qr = a.q.p + (long long)(q0 + r) * a.q.token + pl.hq * a.q.head + 8 * h;
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) q[st] = as_bf16x8(ld16(qr + 16 * st));
   }
@@ -251,8 +220,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
                   char* __restrict__ nextV) {
     const int j0 = kt.at(it);
     if (it + 1 < kt.n) {
-      fetch(nextK, kb, ks, kt.at(it + 1), t.Lk - 1, wave);
-      fetch(nextV, vb, vs, kt.at(it + 1), t.Lk - 1, wave);
+      fetch(nextK, kb, ks, kt.at(it + 1), Lk - 1, wave);
+      fetch(nextV, vb, vs, kt.at(it + 1), Lk - 1, wave);
     }
     if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
       f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
@@ -260,6 +229,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
       for (int st = 0; st < D / 16; ++st)
 #pragma unroll
         for (int b = 0; b < 2; ++b) s[b] = mfma32x32x16(row_frag<D>(K, lo, 32 * b, st), q[st], s[b]);
+      reads_ahead<D / 16, 2, 2, 3>();
       if (!sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -302,8 +272,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
     tiles_ready();
   };
   if (kt.n > 0) {
-    fetch(ldsK0, kb, ks, kt.at(0), t.Lk - 1, wave);
-    fetch(ldsV0, vb, vs, kt.at(0), t.Lk - 1, wave);
+    fetch(ldsK0, kb, ks, kt.at(0), Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(0), Lk - 1, wave);
   }
   tiles_ready();
   for (int it = 0; it < kt.n; it += 2) {
@@ -312,34 +282,35 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, long long slots
   }
   sum += __shfl_xor(sum, 32, kWave);
   if (r0 + n > last) return;
-  store_rows<D>(a.o.p + (long long)(t.q0 + r) * a.o.token + pl.hq * a.o.head, o, sum > 0.f ? 1.f / sum : sum, h);
+  store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + pl.hq * a.o.head, o, sum > 0.f ? 1.f / sum : sum, h);
   if (a.lse != nullptr && h == 0)
-    a.lse[(size_t)pl.hq * a.Tq + t.q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+    a.lse[(size_t)pl.hq * a.Tq + q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
 }
 
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
 // the keys as the forward does.
 template <int D>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, long long slots) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const Place pl = place(a);
-  const QTile t = find_q_tile(a, pl.slot, slots);
+  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
   if (!t.ok) return;
-  const Mask m{t.Lk - t.Lq, a.window, a.sinks};
-  const int last = t.Lq - 1;
-  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.Lk);
+  const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
+  const Mask m{Lk - Lq, a.window, a.sinks};
+  const int last = Lq - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
-  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + pl.hk * a.k.head;
-  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + pl.hk * a.v.head;
+  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + pl.hk * a.v.head;
   bf16x8_t q[D / 16], g[D / 16];
   float delta = 0.f;
   {
-    const long long row = t.q0 + r;
+    const long long row = q0 + r;
     const uint16_t* qr = a.q.p + row * a.q.token + pl.hq * a.q.head + 8 * h;
     const uint16_t* gr = b.dout.p + row * b.dout.token + pl.hq * b.dout.head + 8 * h;
     const uint16_t* orow = a.o.p + row * a.o.token + pl.hq * a.o.head + 8 * h;
@@ -356,8 +327,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
     }
     delta += __shfl_xor(delta, 32, kWave);
   }
-  const size_t stat = (size_t)pl.hq * a.Tq + t.q0 + r;
-  const float lse2 = a.lse[stat] * kLog2e;
+  const size_t stat = (size_t)pl.hq * a.Tq + q0 + r;
+  const float lse = a.lse[stat];
+  const float lse2 = lse > -INFINITY ? lse * kLog2e : 0.f;  // a row that sees nothing: its scores are all -inf
   if (h == 0 && r0 + n <= last) {
     b.lse2[stat] = lse2;
     b.delta[stat] = delta;
@@ -374,8 +346,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
                   char* __restrict__ nextV) {
     const int j0 = kt.at(it);
     if (it + 1 < kt.n) {
-      fetch(nextK, kb, ks, kt.at(it + 1), t.Lk - 1, wave);
-      fetch(nextV, vb, vs, kt.at(it + 1), t.Lk - 1, wave);
+      fetch(nextK, kb, ks, kt.at(it + 1), Lk - 1, wave);
+      fetch(nextV, vb, vs, kt.at(it + 1), Lk - 1, wave);
     }
     if (r0 <= last && !sees_none(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
       const bool all = sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1);
@@ -387,25 +359,28 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
           s = mfma32x32x16(row_frag<D>(K, lo, 32 * blk, st), q[st], s);
           dp = mfma32x32x16(row_frag<D>(V, lo, 32 * blk, st), g[st], dp);
         }
+        reads_ahead<D / 16, 2, 2, 3>();
+        if (!all) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float e = exp2_hw(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-          s[i] = all || m.sees(p, j0 + 32 * blk + acc_row(i, h)) ? e : 0.f;
+          for (int i = 0; i < 16; ++i) s[i] = m.sees(p, j0 + 32 * blk + acc_row(i, h)) ? s[i] : -INFINITY;
         }
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const bf16x8_t df = acc_frag(s, st);
+        for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+        const bf16x8_t df[2] = {acc_frag(s, 0), acc_frag(s, 1)};
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int mb = 0; mb < D / 32; ++mb)
-            dq[mb] = mfma32x32x16(col_frag<D>(K, lo, 32 * blk + 16 * st, mb), df, dq[mb]);
-        }
+            dq[mb] = mfma32x32x16(col_frag<D>(K, lo, 32 * blk + 16 * st, mb), df[st], dq[mb]);
+        reads_ahead<D / 16, 1, 2, 4>();
       }
     }
     tiles_ready();
   };
   if (kt.n > 0) {
-    fetch(ldsK0, kb, ks, kt.at(0), t.Lk - 1, wave);
-    fetch(ldsV0, vb, vs, kt.at(0), t.Lk - 1, wave);
+    fetch(ldsK0, kb, ks, kt.at(0), Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(0), Lk - 1, wave);
   }
   tiles_ready();
   for (int it = 0; it < kt.n; it += 2) {
@@ -413,7 +388,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
     if (it + 1 < kt.n) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   if (r0 + n <= last)
-    store_rows<D>(b.dq.p + (long long)(t.q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
+    store_rows<D>(b.dq.p + (long long)(q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
 }
 
 namespace {
@@ -430,36 +405,24 @@ struct KvTile {
 };
 
 // The tile of place `slot`, or with `sink` set of sinks' tile `slot`.
-__device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool sink, long long slot) {
+__device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool sink, int slots, int slot) {
   const AttnArgs& a = b.f;
   KvTile t{};
-  int s;
-  long long k0;
   if (sink) {
-    s = (int)(slot / b.sink_tiles);
-    k0 = slot % b.sink_tiles * kAttnK;
-  } else if (a.n_seq <= kWave) {  // the longest sequence first, in it the first keys, which the most queries see
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    if (lane < a.n_seq) {
-      const int k0 = min(max(a.kv_off[lane], 0), a.Tkv), k1 = min(max(a.kv_off[lane + 1], 0), a.Tkv);
-      n = (max(k1 - k0, 0) + kAttnK - 1) / kAttnK;
-    }
-    int tile = 0;
-    s = ranked_tile(n, a.n_seq, slot, &tile);
-    if (s < 0) return t;
-    k0 = (long long)tile * kAttnK;
-  } else {
-    s = __builtin_amdgcn_readfirstlane(
-        wave_search(a.n_seq, slot, [&](int i) { return attn_slot0(min(max(a.kv_off[i], 0), a.Tkv), i, kAttnK); }));
-    if (s < 0) return t;
-    k0 = (slot - attn_slot0(min(max(a.kv_off[s], 0), a.Tkv), s, kAttnK)) * kAttnK;
+    const int s = slot / b.sink_tiles;
+    const SeqRange q = seq_range(a.q_off, s, a.Tq), k = seq_range(a.kv_off, s, a.Tkv);
+    t.q = {__builtin_amdgcn_readfirstlane(q.lo), __builtin_amdgcn_readfirstlane(q.n)};
+    t.k = {__builtin_amdgcn_readfirstlane(k.lo), __builtin_amdgcn_readfirstlane(k.n)};
+    t.k0 = slot % b.sink_tiles * kAttnK;
+    if (t.k0 >= t.k.n) return t;
+  } else {  // in a sequence the first keys, which the most queries see, come first
+    const SeqTile f = find_tile<false, false, kAttnK>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, slot);
+    if (!f.ok || f.row0 < b.sink_tiles * kAttnK) return t;
+    t.q = f.a;
+    t.k = f.b;
+    t.k0 = f.row0;
   }
-  t.q = seq_range(a.q_off, s, a.Tq);
-  t.k = seq_range(a.kv_off, s, a.Tkv);
-  if (k0 < 0 || k0 >= t.k.n || (!sink && k0 < (long long)b.sink_tiles * kAttnK)) return t;
   t.ok = true;
-  t.k0 = (int)k0;
   const int shift = t.k.n - t.q.n, group = a.Hq / a.Hkv;
   const int i_lo = max(t.k0 - shift, 0);
   int i_hi = t.q.n;
@@ -474,7 +437,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
   t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, kAttnMinSteps);
   t.chunks = max((t.total + t.per - 1) / t.per, 1);
   const long long sink_parts = (long long)b.sink_tiles * a.n_seq * b.sink_splits;
-  t.part = sink ? slot * splits : sink_parts + slot * splits;
+  t.part = (sink ? 0 : sink_parts) + (long long)slot * splits;
   return t;
 }
 
@@ -485,7 +448,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
 // dP are computed with the queries down, so that P and dS are the right operands of dV^T = dO^T P
 // and dK^T = Q^T dS.
 template <int D>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, long long slots) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBQ * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
   __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
@@ -499,14 +462,12 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardA
   const int group = a.Hq / a.Hkv;
   // The sinks' tiles come first.  The chunk is the slowest index: workgroups without work then lie
   // together at the end (spread between the others they would leave whole CUs idle).
-  const int hk = (int)(blockIdx.x % a.Hkv);
-  long long id = blockIdx.x / a.Hkv;
-  const long long sinks = (long long)b.sink_tiles * a.n_seq, first = sinks * b.sink_splits;
+  const int hk = (int)(blockIdx.x % a.Hkv), sinks = b.sink_tiles * a.n_seq, first = sinks * b.sink_splits;
+  int id = (int)(blockIdx.x / a.Hkv);
   const bool sink = id < first;
   if (!sink) id -= first;
-  const long long n_tiles = sink ? sinks : slots;
-  const int chunk = (int)(id / n_tiles);
-  const KvTile t = find_kv_tile(b, sink, id % n_tiles);
+  const int n_tiles = sink ? sinks : slots, chunk = id / n_tiles;
+  const KvTile t = find_kv_tile(b, sink, slots, id - chunk * n_tiles);
   if (!t.ok || chunk >= t.chunks) return;
   const SeqRange qr = t.q, kr = t.k;
   const int k0 = t.k0, Lq = qr.n, Lk = kr.n, nt = t.nt;
@@ -560,28 +521,35 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardA
         s = mfma32x32x16(row_frag<D>(Q, lo, 0, st), kf[st], s);
         dp = mfma32x32x16(row_frag<D>(G, lo, 0, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
       }
+      reads_ahead<D / 16, 2, 3, 3>();
+      if (!all) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = i0 + acc_row(i, h);
+          s[i] = row < Lq && m.sees(row + m.shift, j) ? s[i] : -INFINITY;
+        }
+      }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + 8 * g + 4 * h);
         const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + 8 * g + 4 * h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = i0 + 8 * g + 4 * h + i;
-          const bool on = all || (row < Lq && m.sees(row + m.shift, j));
-          const float pv = on ? exp2_hw(fmaf(s[4 * g + i], c, -l4[i])) : 0.f;
+          const float pv = exp2_hw(fmaf(s[4 * g + i], c, -l4[i]));
           s[4 * g + i] = pv;
-          dp[4 * g + i] = on ? pv * (dp[4 * g + i] - d4[i]) : 0.f;
+          dp[4 * g + i] = pv * (dp[4 * g + i] - d4[i]);
         }
       }
+      const bf16x8_t pf[2] = {acc_frag(s, 0), acc_frag(s, 1)}, df[2] = {acc_frag(dp, 0), acc_frag(dp, 1)};
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const bf16x8_t pf = acc_frag(s, st), df = acc_frag(dp, st);
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int mb = 0; mb < D / 32; ++mb) {
-          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pf, dv[mb]);
-          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), df, dk[mb]);
+          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pf[st], dv[mb]);
+          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), df[st], dk[mb]);
         }
-      }
+      reads_ahead<D / 8, 1, 2, 4>();
     }
     tiles_ready();
   };
@@ -618,11 +586,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardA
 // Adds the chunks of the key tiles that were split, in order: kJoinParts workgroups per tile.
 constexpr int kJoinParts = 16;
 template <int D>
-__global__ __launch_bounds__(256) void attn_dkv_join_k(AttnBackwardArgs b) {
+__global__ __launch_bounds__(256) void attn_dkv_join_k(AttnBackwardArgs b, int slots) {
   const AttnArgs& a = b.f;
   const int hk = (int)(blockIdx.x % a.Hkv), piece = (int)(blockIdx.x / a.Hkv % kJoinParts);
-  const long long id = blockIdx.x / a.Hkv / kJoinParts, sinks = (long long)b.sink_tiles * a.n_seq;
-  const KvTile t = find_kv_tile(b, id < sinks, id < sinks ? id : id - sinks);
+  const int id = (int)(blockIdx.x / a.Hkv / kJoinParts), sinks = b.sink_tiles * a.n_seq;
+  const KvTile t = find_kv_tile(b, id < sinks, slots, id < sinks ? id : id - sinks);
   if (!t.ok || t.chunks == 1) return;
   const float* part = b.part + ((size_t)t.part * a.Hkv + hk) * attn_part_floats(D);
   const size_t next = (size_t)a.Hkv * attn_part_floats(D);
@@ -648,7 +616,7 @@ namespace {
 template <int D>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
   const long long slots = attn_slots(a.Tq, a.n_seq, kAttnQ);
-  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 0, s, a, slots);
+  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 0, s, a, (int)slots);
   return hipGetLastError();
 }
 
@@ -657,17 +625,17 @@ hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
   const AttnArgs& a = b.f;
   const long long qs = attn_slots(a.Tq, a.n_seq, kAttnQ), ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
   if (a.Tq > 0) {
-    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 0, s, b, qs);
+    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 0, s, b, (int)qs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const long long sinks = (long long)b.sink_tiles * a.n_seq;
   hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,
-                     ks);
+                     (int)ks);
   const hipError_t e = hipGetLastError();
   const long long joins = sinks + (b.splits > 1 ? ks : 0);
   if (e != hipSuccess || joins == 0) return e;
-  hipLaunchKernelGGL((attn_dkv_join_k<D>), dim3((unsigned)(joins * a.Hkv * kJoinParts)), dim3(256), 0, s, b);
+  hipLaunchKernelGGL((attn_dkv_join_k<D>), dim3((unsigned)(joins * a.Hkv * kJoinParts)), dim3(256), 0, s, b, (int)ks);
   return hipGetLastError();
 }
 

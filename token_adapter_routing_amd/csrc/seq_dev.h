@@ -38,30 +38,83 @@ __device__ __forceinline__ int wave_search(int n, long long x, Key key) {
   }
 }
 
-// Tiles of up to 64 sequences, the longest sequence first: lane s holds sequence s's number of tiles
-// (0 past the last).  The sequence of the rank-th tile, -1 past the last, and in *tile its place in
-// the sequence.
-__device__ __forceinline__ int ranked_tile(int n, int n_seq, long long rank, int* tile) {
-  const int lane = threadIdx.x & 63;
-  long long first = 0;  // tiles of the sequences before this one
-  for (int s = 0; s < n_seq; ++s) {
-    const int m = __builtin_amdgcn_readlane(n, s);
-    if (m > n || (m == n && s < lane)) first += m;
-  }
-  const uint64_t mine = __ballot(n > 0 && first <= rank && rank < first + n);
-  if (mine == 0) return -1;
-  const int s = __builtin_ctzll(mine);
-  *tile = __builtin_amdgcn_readlane((int)(rank - first), s);
-  return s;
-}
-
-// Row range of sequence s, limited to [0, T].
+// Row range of one sequence, limited to [0, T].
 struct SeqRange {
   int lo, n;
 };
 __device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ off, int s, int T) {
   const int a = min(max(off[s], 0), T), b = min(max(off[s + 1], 0), T);
-  return {__builtin_amdgcn_readfirstlane(a), __builtin_amdgcn_readfirstlane(max(b - a, 0))};
+  return {a, max(b - a, 0)};
+}
+
+// The tile of one slot of a packed batch, tiles of `tile` rows of the first or the second of two
+// offset arrays: sequence, first row in it, both row ranges.
+struct SeqTile {
+  int s, row0;
+  SeqRange a, b;
+  bool ok;
+};
+
+// kRanked sequences at most: the longest sequence's tiles come first (workgroups start in slot order, so
+// long ones do not come last), FROM_END: its last tile first.  The search is a step per sequence,
+// which with more would cost what the order gains (32 sequences of 512 tokens: 83 us in slot order,
+// 98 us ranked).
+// With more, slots run through the sequences (attn_slot0).  Up to 64 the lanes hold one each.
+constexpr int kRanked = 16;
+template <bool OF_A, bool FROM_END, int TILE>
+__device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ offa, int Ta, const int32_t* __restrict__ offb,
+                                             int Tb, int n_seq, int slots, int slot) {
+  SeqTile t{};
+  if (n_seq > kWave) {
+    if (FROM_END) slot = slots - 1 - slot;
+    const int32_t* off = OF_A ? offa : offb;
+    const int T = OF_A ? Ta : Tb;
+    const int s = __builtin_amdgcn_readfirstlane(
+        wave_search(n_seq, slot, [&](int i) { return attn_slot0(min(max(off[i], 0), T), i, TILE); }));
+    if (s < 0) return t;
+    const SeqRange a = seq_range(offa, s, Ta), b = seq_range(offb, s, Tb);
+    t.a = {__builtin_amdgcn_readfirstlane(a.lo), __builtin_amdgcn_readfirstlane(a.n)};
+    t.b = {__builtin_amdgcn_readfirstlane(b.lo), __builtin_amdgcn_readfirstlane(b.n)};
+    t.s = s;
+    const long long row0 = (slot - attn_slot0(OF_A ? t.a.lo : t.b.lo, s, TILE)) * TILE;
+    t.ok = row0 >= 0 && row0 < (OF_A ? t.a.n : t.b.n);
+    t.row0 = (int)row0;
+    return t;
+  }
+  const int lane = threadIdx.x & 63;
+  SeqRange a{0, 0}, b{0, 0};
+  if (lane < n_seq) {
+    a = seq_range(offa, lane, Ta);
+    b = seq_range(offb, lane, Tb);
+  }
+  const SeqRange mine = OF_A ? a : b;
+  const int n = (mine.n + TILE - 1) / TILE;
+  int s, tile;
+  if (n_seq <= kRanked) {
+    int first = 0;  // tiles of the sequences before this one
+    for (int i = 0; i < n_seq; ++i) {
+      const int m = __builtin_amdgcn_readlane(n, i);
+      first += (m > n || (m == n && i < lane)) ? m : 0;
+    }
+    const uint64_t here = __ballot(first <= slot && slot < first + n);
+    if (here == 0) return t;
+    s = __builtin_ctzll(here);
+    tile = slot - __builtin_amdgcn_readlane(first, s);
+    if (FROM_END) tile = __builtin_amdgcn_readlane(n, s) - 1 - tile;
+  } else {
+    if (FROM_END) slot = slots - 1 - slot;
+    const int first = (int)attn_slot0(mine.lo, lane, TILE);
+    const uint64_t here = __ballot(lane < n_seq && first <= slot && slot < first + n);
+    if (here == 0) return t;
+    s = __builtin_ctzll(here);
+    tile = slot - __builtin_amdgcn_readlane(first, s);
+  }
+  t.s = s;
+  t.row0 = tile * TILE;
+  t.a = {__builtin_amdgcn_readlane(a.lo, s), __builtin_amdgcn_readlane(a.n, s)};
+  t.b = {__builtin_amdgcn_readlane(b.lo, s), __builtin_amdgcn_readlane(b.n, s)};
+  t.ok = true;
+  return t;
 }
 
 // What the queries of one sequence see.
