@@ -189,10 +189,8 @@ __global__ __launch_bounds__(256, 2) void attn_decode_k(DecodeArgs a, int head_t
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15,
             g = lane >> 4;
   // consecutive workgroups take different sequences and heads: a long sequence's splits spread
-  const long long units = (long long)a.n_seq * a.c.Hkv * head_tiles;
-  const int split = (int)(blockIdx.x / units);
-  const long long unit = blockIdx.x % units;
-  const int ht = (int)(unit % head_tiles), hk = (int)(unit / head_tiles % a.c.Hkv),
+  const unsigned units = (unsigned)a.n_seq * a.c.Hkv * head_tiles, unit = blockIdx.x % units;
+  const int split = (int)(blockIdx.x / units), ht = (int)(unit % head_tiles), hk = (int)(unit / head_tiles % a.c.Hkv),
             b = (int)(unit / head_tiles / a.c.Hkv);
   const DecSeq sq = dec_seq(a, b);
   const int per = decode_blocks_per_split(sq.blocks, a.splits);
@@ -359,44 +357,59 @@ __global__ __launch_bounds__(256, 2) void attn_decode_k(DecodeArgs a, int head_t
   }
 }
 
-// Joins the splits of one (sequence, query head): a wave each, split by split in order.
+// Joins the splits of one (sequence, query head): a workgroup each, D / 4 threads per part, so that 8
+// or 16 parts are read side by side; each such group of threads adds its parts in order, then the
+// groups' sums are added in order.
 template <int D>
 __global__ __launch_bounds__(256) void attn_decode_join_k(DecodeArgs a, int head_tiles) {
-  const int lane = threadIdx.x & 63;
-  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= (long long)a.n_seq * a.Hq) return;
-  const int b = __builtin_amdgcn_readfirstlane((int)(id / a.Hq)), hq = __builtin_amdgcn_readfirstlane((int)(id % a.Hq));
+  constexpr int kThreads = D / 4, kGroups = 256 / kThreads;
+  __shared__ float maxima[4];
+  __shared__ __attribute__((aligned(16))) float sums[kGroups][D + 4];  // and l behind each
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const unsigned id = blockIdx.x;
+  const int b = (int)(id / a.Hq), hq = (int)(id % a.Hq);
   const int group = a.Hq / a.c.Hkv, hk = hq / group, ht = hq % group / kDecHeads, head = hq % group % kDecHeads;
   const DecSeq sq = dec_seq(a, b);
   const int per = decode_blocks_per_split(sq.blocks, a.splits);
   const int parts = max(1, (sq.blocks + per - 1) / per);
-  const size_t unit = ((size_t)b * a.c.Hkv + hk) * head_tiles + ht;
-  const float* part = a.part + unit * a.splits * decode_part_floats(D);
-  constexpr int E = D / kWave;
+  const size_t unit = ((size_t)b * a.c.Hkv + hk) * head_tiles + ht, next = decode_part_floats(D);
+  const float* part = a.part + unit * a.splits * next;
   float m = -INFINITY;
-  for (int s = lane; s < parts; s += kWave) m = fmaxf(m, part[s * decode_part_floats(D) + kDecHeads * D + head]);
+  for (int s = tid; s < parts; s += 256) m = fmaxf(m, part[s * next + kDecHeads * D + head]);
   m = wave_max(m);
+  if (lane == 0) maxima[wave] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
   const float ref = m > -INFINITY ? m : 0.f;
-  float l = 0.f, r[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) r[j] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float* ps = part + s * decode_part_floats(D);
+  const int grp = tid / kThreads, d0 = tid % kThreads * 4;
+  float l = 0.f;
+  f32x4_t r{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int s = grp; s < parts; s += kGroups) {
+    const float* ps = part + s * next;
     const float f = exp2_hw(ps[kDecHeads * D + head] - ref);
     l = fmaf(ps[kDecHeads * (D + 1) + head], f, l);
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ps + head * D + d0);
 #pragma unroll
-    for (int j = 0; j < E; ++j) r[j] = fmaf(ps[head * D + E * lane + j], f, r[j]);
+    for (int j = 0; j < 4; ++j) r[j] = fmaf(x[j], f, r[j]);
+  }
+  *reinterpret_cast<f32x4_t*>(&sums[grp][d0]) = r;
+  if (d0 == 0) sums[grp][D] = l;
+  __syncthreads();
+  if (tid >= kThreads) return;
+  l = 0.f;
+  r = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    l += sums[g][D];
+    r += *reinterpret_cast<const f32x4_t*>(&sums[g][d0]);
   }
   const float inv = l > 0.f ? 1.f / l : l;
-  uint16_t* po = a.o.p + b * a.o.token + hq * a.o.head + E * lane;
-  if constexpr (E == 2) {
-    *reinterpret_cast<uint32_t*>(po) = pack_bf16x2(r[0] * inv, r[1] * inv);
-  } else {
-    const __bf16 v = (__bf16)(r[0] * inv);
-    *po = __builtin_bit_cast(uint16_t, v);
-  }
-  if (a.lse != nullptr && lane == 0)
+  uint2 v;
+  v.x = pack_bf16x2(r[0] * inv, r[1] * inv);
+  v.y = pack_bf16x2(r[2] * inv, r[3] * inv);
+  *reinterpret_cast<uint2*>(a.o.p + b * a.o.token + hq * a.o.head + d0) = v;
+  if (a.lse != nullptr && tid == 0)
     a.lse[(size_t)b * a.Hq + hq] = l > 0.f ? (m + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
 }
 
@@ -410,8 +423,7 @@ hipError_t decode(const DecodeArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((attn_decode_k<D, false>), grid, dim3(256), 0, s, a, head_tiles);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((attn_decode_join_k<D>), dim3((unsigned)(((long long)a.n_seq * a.Hq + 3) / 4)), dim3(256), 0, s, a,
-                     head_tiles);
+  hipLaunchKernelGGL((attn_decode_join_k<D>), dim3((unsigned)(a.n_seq * a.Hq)), dim3(256), 0, s, a, head_tiles);
   return hipGetLastError();
 }
 

@@ -24,16 +24,43 @@ constexpr int kLanes = 8;             // lanes per token
 constexpr int kTok = kWave / kLanes;  // tokens per wave
 constexpr int kWaves = 4;             // waves per workgroup
 
+// The value of another lane of the eight: STEP 0 lane ^ 1, 1 lane ^ 2, 2 the mirrored lane (which after
+// the first two steps holds what lane ^ 4 holds).  Register moves, no LDS exchange.
+template <int STEP>
+__device__ __forceinline__ int peer(int v) {
+  constexpr int kCtrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : 0x141;  // quad_perm 1032, 2301; row_half_mirror
+  return __builtin_amdgcn_update_dpp(v, v, kCtrl, 0xf, 0xf, true);
+}
+template <int STEP>
+__device__ __forceinline__ float peer(float v) {
+  return __int_as_float(peer<STEP>(__float_as_int(v)));
+}
+template <int STEP>
+__device__ __forceinline__ double peer(double v) {
+  const uint64_t u = __double_as_longlong(v);
+  const uint32_t lo = peer<STEP>((int)(uint32_t)u), hi = peer<STEP>((int)(uint32_t)(u >> 32));
+  return __longlong_as_double(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+
+// Reductions over the eight lanes of a token, the result in all of them.
 template <typename F>
 __device__ __forceinline__ F sum8(F v) {
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
+  v += peer<0>(v);
+  v += peer<1>(v);
+  return v + peer<2>(v);
 }
-__device__ __forceinline__ float max8(float v) {
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
-  return v;
+template <typename F>
+__device__ __forceinline__ F max8(F v) {
+  v = larger(v, peer<0>(v));
+  v = larger(v, peer<1>(v));
+  return larger(v, peer<2>(v));
+}
+__device__ __forceinline__ int min8(int v) {
+  v = min(v, peer<0>(v));
+  v = min(v, peer<1>(v));
+  return min(v, peer<2>(v));
 }
 
 // Lane's E logits of token `tok`; absent adapters (NaN, -inf, past K) come as -inf, +inf as the
@@ -102,34 +129,22 @@ __device__ __forceinline__ uint64_t take_largest(F* v, int base, int step, int r
   F last = INFINITY;
   *gap = INFINITY;
   for (int r = 0; r <= rounds; ++r) {
-    F best = -INFINITY;
-    int at = 64;
+    F best = v[0];
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (v[j] > best) {
-        best = v[j];
-        at = base + j * step;
-      }
-#pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) {
-      const F ov = __shfl_xor(best, d, kWave);
-      const int oa = __shfl_xor(at, d, kWave);
-      if (ov > best || (ov == best && oa < at)) {
-        best = ov;
-        at = oa;
-      }
-    }
+    for (int j = 1; j < E; ++j) best = larger(best, v[j]);
+    best = max8(best);
     if (r == rounds) {
       if (best > -INFINITY) *gap = last - best;
       break;
     }
     last = best;
-    if (best > -INFINITY) {
-      taken |= 1ull << at;
+    int at = 64;
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (base + j * step == at) v[j] = -INFINITY;
-    }
+    for (int j = E - 1; j >= 0; --j) at = v[j] == best ? base + j * step : at;
+    at = min8(at);
+    if (best > -INFINITY) taken |= 1ull << at;
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = base + j * step == at ? -INFINITY : v[j];
   }
   return taken;
 }
