@@ -47,7 +47,7 @@ struct DecodePlan {
 DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int page_size, int table_width);
 MOLORA_HD inline size_t decode_part_floats(int head_dim) { return (size_t)kDecHeads * (head_dim + 2); }
 MOLORA_HD inline int decode_blocks_per_split(int blocks, int splits) {
-  const int per = (blocks + splits - 1) / splits;
+  const int per = ((blocks + splits - 1) / splits + 3) / 4 * 4;  // the four waves take as many each
   return per < kDecMinBlocks ? kDecMinBlocks : per;
 }
 

@@ -363,9 +363,8 @@ __global__ __launch_bounds__(256, 2) void attn_decode_k(DecodeArgs a, int head_t
 template <int D>
 __global__ __launch_bounds__(256) void attn_decode_join_k(DecodeArgs a, int head_tiles) {
   constexpr int kThreads = D / 4, kGroups = 256 / kThreads;
-  __shared__ float maxima[4];
-  __shared__ __attribute__((aligned(16))) float sums[kGroups][D + 4];  // and l behind each
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) float sums[kGroups][D + 4];  // behind each l and m
+  const int tid = threadIdx.x;
   const unsigned id = blockIdx.x;
   const int b = (int)(id / a.Hq), hq = (int)(id % a.Hq);
   const int group = a.Hq / a.c.Hkv, hk = hq / group, ht = hq % group / kDecHeads, head = hq % group % kDecHeads;
@@ -374,35 +373,59 @@ __global__ __launch_bounds__(256) void attn_decode_join_k(DecodeArgs a, int head
   const int parts = max(1, (sq.blocks + per - 1) / per);
   const size_t unit = ((size_t)b * a.c.Hkv + hk) * head_tiles + ht, next = decode_part_floats(D);
   const float* part = a.part + unit * a.splits * next;
-  float m = -INFINITY;
-  for (int s = tid; s < parts; s += 256) m = fmaxf(m, part[s * next + kDecHeads * D + head]);
-  m = wave_max(m);
-  if (lane == 0) maxima[wave] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
-  const float ref = m > -INFINITY ? m : 0.f;
+  // a group's parts eight at a time, with their own reference maximum
   const int grp = tid / kThreads, d0 = tid % kThreads * 4;
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   f32x4_t r{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = grp; s < parts; s += kGroups) {
-    const float* ps = part + s * next;
-    const float f = exp2_hw(ps[kDecHeads * D + head] - ref);
-    l = fmaf(ps[kDecHeads * (D + 1) + head], f, l);
-    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ps + head * D + d0);
+  for (int s0 = grp; s0 < parts; s0 += 8 * kGroups) {
+    float pm[8], pl[8];
+    f32x4_t x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = fmaf(x[j], f, r[j]);
+    for (int i = 0; i < 8; ++i) {
+      const float* ps = part + min(s0 + i * kGroups, parts - 1) * next;
+      pm[i] = ps[kDecHeads * D + head];
+      pl[i] = ps[kDecHeads * (D + 1) + head];
+      x[i] = *reinterpret_cast<const f32x4_t*>(ps + head * D + d0);
+    }
+    float up = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i * kGroups >= parts) pm[i] = -INFINITY;
+      up = fmaxf(up, pm[i]);
+    }
+    const float ref = up > -INFINITY ? up : 0.f, f0 = exp2_hw(m - ref);
+    m = up;
+    l *= f0;
+    r *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i * kGroups >= parts) continue;  // a repeated part: whatever it holds stays out
+      const float f = exp2_hw(pm[i] - ref);
+      l = fmaf(pl[i], f, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = fmaf(x[i][j], f, r[j]);
+    }
   }
   *reinterpret_cast<f32x4_t*>(&sums[grp][d0]) = r;
-  if (d0 == 0) sums[grp][D] = l;
+  if (d0 == 0) {
+    sums[grp][D] = l;
+    sums[grp][D + 1] = m;
+  }
   __syncthreads();
   if (tid >= kThreads) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sums[g][D + 1]);
+  const float ref = m > -INFINITY ? m : 0.f;
   l = 0.f;
   r = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    l += sums[g][D];
-    r += *reinterpret_cast<const f32x4_t*>(&sums[g][d0]);
+    const float f = exp2_hw(sums[g][D + 1] - ref);
+    l = fmaf(sums[g][D], f, l);
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(&sums[g][d0]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = fmaf(x[j], f, r[j]);
   }
   const float inv = l > 0.f ? 1.f / l : l;
   uint2 v;

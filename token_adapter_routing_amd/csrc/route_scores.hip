@@ -43,6 +43,8 @@ __device__ __forceinline__ double peer(double v) {
 }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
 
 // Reductions over the eight lanes of a token, the result in all of them.
 template <typename F>
@@ -156,32 +158,38 @@ __device__ __forceinline__ uint64_t choose(F* c, const RouteScoresArgs& a, int t
   *margin = INFINITY;
   if (a.n_group > 1) {
     const int gs = a.K / a.n_group;
-    F* row = mem + t * a.K;
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (lane8 * E + j < a.K) row[lane8 * E + j] = c[j];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    F mark[8];  // groups lane8, lane8 + 8, ...
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mark[i] = -INFINITY;
-      const int g = lane8 + kLanes * i;
-      if (g >= a.n_group) continue;
+    // a group's mark: its largest value plus its second largest where it has one
+    auto add = [](F& m1, F& m2, F x) {
+      m2 = larger(m2, smaller(m1, x));
+      m1 = larger(m1, x);
+    };
+    auto mark_of = [](F m1, F m2) { return m2 > -INFINITY ? m1 + m2 : m1; };
+    uint64_t kept;
+    if (gs == E) {  // a lane's adapters are a group
       F m1 = -INFINITY, m2 = -INFINITY;
-      for (int j = 0; j < gs; ++j) {
-        const F x = row[g * gs + j];
-        if (x > m1) {
-          m2 = m1;
-          m1 = x;
-        } else if (x > m2) {
-          m2 = x;
-        }
+#pragma unroll
+      for (int j = 0; j < E; ++j) add(m1, m2, c[j]);
+      F mark[1] = {mark_of(m1, m2)};
+      kept = take_largest<F, 1>(mark, lane8, 1, a.topk_group, margin);
+    } else {
+      F* row = mem + t * a.K;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (lane8 * E + j < a.K) row[lane8 * E + j] = c[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      F mark[8];  // groups lane8, lane8 + 8, ...
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        F m1 = -INFINITY, m2 = -INFINITY;
+        const int g = lane8 + kLanes * i;
+        if (g < a.n_group)
+          for (int j = 0; j < gs; ++j) add(m1, m2, row[g * gs + j]);
+        mark[i] = mark_of(m1, m2);
       }
-      mark[i] = m2 > -INFINITY ? m1 + m2 : m1;
+      kept = take_largest<F, 8>(mark, lane8, kLanes, a.topk_group, margin);
     }
-    const uint64_t kept = take_largest<F, 8>(mark, lane8, kLanes, a.topk_group, margin);
     const uint32_t inv = (65536u + gs - 1) / gs;  // e / gs for e < 64
 #pragma unroll
     for (int j = 0; j < E; ++j) {
