@@ -96,14 +96,17 @@ int molora_route_scores_backward(const float *logits, const int32_t *idx, const 
  * may reach any output row of its sequence.
  * Products are bf16 with fp32 accumulation; the softmax runs in fp32 and its
  * weights enter the second product as bf16; o is rounded once at the store.
+ * Where few query rows face many keys the keys are split over workgroups and
+ * a second launch joins the parts.
+ *   ws      device workspace of the call's *_workspace() bytes (which read the
+ *           shape's numbers, not its pointers), 256-byte aligned, no initial
+ *           contents (size 0: may be NULL); calls that share it must not
+ *           overlap
  *
  * molora_attn_backward: dq, dk, dv (laid out as molora_rows like q, k, v) from
  * do = dL/do and the forward's o and lse.  Gradients of shared key-value heads
  * are summed in fp32 over their query heads.  Rows outside every sequence are
  * left as they were; rows that nothing sees get 0.
- *   ws      device workspace of molora_attn_backward_workspace() bytes,
- *           256-byte aligned, no initial contents; calls that share it must
- *           not overlap
  * Supported: head_dim 64 or 128, 1 <= n_kv_heads, n_heads a multiple of it and
  * at most 1024, n_seq, Tq, Tkv >= 0 and below 2^24, token strides below 2^23,
  * scale positive and finite, sinks <= 2^24.
@@ -122,8 +125,10 @@ typedef struct {
   int window, sinks;
   float scale;
 } molora_attn_shape;
+int molora_attn_forward_workspace(const molora_attn_shape *shape, size_t *bytes);
 int molora_attn_forward(const molora_attn_shape *shape, const molora_rows *q, const molora_rows *k,
-                        const molora_rows *v, const molora_rows *o, float *lse, void *stream);
+                        const molora_rows *v, const molora_rows *o, float *lse, void *ws,
+                        size_t ws_bytes, void *stream);
 int molora_attn_backward_workspace(const molora_attn_shape *shape, size_t *bytes);
 int molora_attn_backward(const molora_attn_shape *shape, const molora_rows *dout, const molora_rows *q,
                          const molora_rows *k, const molora_rows *v, const molora_rows *o,

@@ -77,10 +77,10 @@ def shape(**kw):
     return D.MoloraAttnShape(*a.values())
 
 
-def attn(s=None, q=None, k=None, v=None, o=None, lse=FAKE):
+def attn(s=None, q=None, k=None, v=None, o=None, lse=FAKE, ws=None, size=0):
     r = ctypes.byref
     return lib().molora_attn_forward(r(s or shape()), r(q or rows(512, 64)), r(k or rows(128, 64)),
-                                     r(v or rows(128, 64)), r(o or rows(512, 64)), lse, None)
+                                     r(v or rows(128, 64)), r(o or rows(512, 64)), lse, ws, size, None)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -94,6 +94,7 @@ def test_attention_shape_refusals(change, code):
     assert attn(shape(**change)) == code, last()
     n = ctypes.c_size_t()
     assert lib().molora_attn_backward_workspace(ctypes.byref(shape(**change)), ctypes.byref(n)) == code
+    assert lib().molora_attn_forward_workspace(ctypes.byref(shape(**change)), ctypes.byref(n)) == code
 
 
 @pytest.mark.parametrize("which,bad,code", [
@@ -110,6 +111,17 @@ def test_attention_misaligned_lse_and_empty_calls():
     assert attn(lse=FAKE + 2) == EINVAL
     assert attn(shape(Tq=0), q=rows(512, 64, None), o=rows(512, 64, None)) == 0
     assert attn(shape(n_seq=0, q_off=None)) == 0
+
+
+def test_attention_forward_workspace():
+    r, n = ctypes.byref, ctypes.c_size_t()
+    assert lib().molora_attn_forward_workspace(r(shape()), None) == EINVAL
+    assert lib().molora_attn_forward_workspace(r(shape()), r(n)) == 0 and n.value == 0  # few keys: nothing to split
+    few = shape(Tkv=5000)
+    assert lib().molora_attn_forward_workspace(r(few), r(n)) == 0 and n.value > 0 and n.value % 256 == 0
+    assert attn(few) == ENOSPC and attn(few, ws=FAKE, size=n.value - 1) == ENOSPC
+    assert attn(few, ws=FAKE + 64, size=n.value) == ENOSPC
+    assert lib().molora_attn_forward_workspace(r(shape(Tkv=5000, Tq=100000)), r(n)) == 0 and n.value == 0
 
 
 def test_attention_backward_workspace_and_refusals():

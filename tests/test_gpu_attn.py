@@ -108,6 +108,55 @@ def test_queries_behind_earlier_keys(q_lens, kv_lens):
     run(need_gpu(), Case(q_lens, kv_lens, 4, 2, 128, seed=9))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens,window,sinks", [
+    ([1], [2000], 0, 0), ([20], [1500], 0, 0), ([130, 0, 7], [1000, 50, 2100], 0, 0), ([800], [800], 0, 0),
+    ([33], [1700], 900, 0), ([33], [1700], 500, 70), ([900, 40], [20, 1600], 0, 0)])
+def test_keys_split_over_workgroups(q_lens, kv_lens, window, sinks, D):
+    """Few query rows before many keys: parts and their join, forward and backward."""
+    m = need_gpu()
+    c = Case(q_lens, kv_lens, 4, 2, D, window=window, sinks=sinks, seed=30)
+    assert m.molora_attn_forward_workspace(c.q.cuda(), c.k.cuda(), c.off()[0], window, sinks) > 0
+    a, b = run(m, c), run(m, c)
+    for x, y in zip((a[0], a[1], *a[2]), (b[0], b[1], *b[2])):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("n_seq", [15, 16, 17, 63, 64, 65, 200])
+def test_numbers_of_sequences(n_seq):
+    """Tiles are found in three ways, by the number of sequences."""
+    lens = [(i * 53) % 190 for i in range(n_seq)]
+    kv = [n + (i * 31) % 70 if n else 0 for i, n in enumerate(lens)]
+    run(need_gpu(), Case(lens, kv, 2, 1, 64, window=40, sinks=3, seed=n_seq))
+    run(need_gpu(), Case(lens, kv, 1, 1, 64, seed=n_seq))
+
+
+def test_key_tiles_split_into_chunks():
+    """Long sequences of few heads: the backward's key tiles in chunks, a window's sinks apart."""
+    run(need_gpu(), Case([2500, 0, 1100], [2500, 9, 1300], 2, 1, 64, seed=31))
+    run(need_gpu(), Case([2500, 0, 1100], [2500, 9, 1300], 4, 1, 64, window=200, sinks=150, seed=32))
+    run(need_gpu(), Case([1600], [1600], 4, 1, 128, window=300, sinks=5, seed=33))
+
+
+def test_workspace_given():
+    m = need_gpu()
+    c = Case([20], [1500], 4, 2, 64, seed=34)
+    q, k, v, do = (x.cuda() for x in (c.q, c.k, c.v, c.do))
+    q_off, kv_off = c.off()
+    ws = torch.full((m.molora_attn_forward_workspace(q, k, q_off) + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    o, lse = m.molora_attn_forward(q, k, v, q_off, kv_off, ws=ws)  # whatever it holds
+    check_forward(c, o, lse)
+    assert (ws[-512:] == 0xFF).all()
+    n = m.molora_attn_backward_workspace(q, k, q_off)
+    wb = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    check_backward(c, o, lse, m.molora_attn_backward(do, q, k, v, o, lse, q_off, kv_off, ws=wb))
+    assert (wb[n:] == 0xFF).all()
+    with pytest.raises(m.MoloraError, match="workspace"):
+        m.molora_attn_forward(q, k, v, q_off, kv_off, ws=ws[:256])
+    with pytest.raises(m.MoloraError, match="workspace"):
+        m.molora_attn_backward(do, q, k, v, o, lse, q_off, kv_off, ws=wb[:256])
+
+
 @pytest.mark.parametrize("q_lens,kv_lens", [([40], [10]), ([200, 5], [3, 0]), ([130], [129]), ([300], [140])])
 @pytest.mark.parametrize("window", [0, 7])
 def test_rows_that_see_nothing(q_lens, kv_lens, window):

@@ -19,6 +19,6 @@ from .binding import (  # noqa: F401
 from .decoder import (  # noqa: F401
     E4M3, SCORE_SIGMOID, SCORE_SOFTMAX, KvCache, decoder_symbols,
     molora_attn_backward, molora_attn_backward_workspace, molora_attn_decode, molora_attn_decode_workspace,
-    molora_attn_forward, molora_kv_append, molora_route_scores, molora_route_scores_backward,
+    molora_attn_forward, molora_attn_forward_workspace, molora_kv_append, molora_route_scores, molora_route_scores_backward,
     molora_xf_decode, molora_xf_prefill, molora_xf_serve_workspace,
 )

@@ -157,14 +157,39 @@ __device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int 
   return j1 <= p_lo && (!m.window || j0 > p_hi - m.window || j1 < m.sinks);
 }
 
-// Workgroup -> (head, slot): the heads of one key-value head follow each other on one XCD
-// (consecutive workgroups go round the XCDs).
+// Workgroup -> (head, slot, chunk of the slot's key tiles): the heads of one key-value head follow each
+// other on one XCD (consecutive workgroups go round the XCDs); the chunk is the slowest, so that
+// workgroups without work lie together at the end.
 struct Place {
-  int hq, hk, slot;
+  int hq, hk, slot, chunk;
 };
-__device__ __forceinline__ Place place(const AttnArgs& a) {
-  const unsigned g = a.Hq / a.Hkv, id = blockIdx.x, rest = id / a.Hkv, hk = id % a.Hkv;
-  return {(int)(hk * g + rest % g), (int)hk, (int)(rest / g)};
+__device__ __forceinline__ Place place(const AttnArgs& a, int slots) {
+  const unsigned g = a.Hq / a.Hkv, id = blockIdx.x, rest = id / a.Hkv, hk = id % a.Hkv, at = rest / g;
+  const unsigned chunk = at / slots;
+  return {(int)(hk * g + rest % g), (int)hk, (int)(at - chunk * slots), (int)chunk};
+}
+
+// A query tile's key tiles split over up to `splits` workgroups, at least kAttnMinTiles each.
+struct Chunks {
+  int per, n;
+};
+__device__ __forceinline__ Chunks key_chunks(int tiles, int splits) {
+  const int per = max((tiles + splits - 1) / splits, kAttnMinTiles);
+  return {per, max((tiles + per - 1) / per, 1)};
+}
+
+// Stores a 32 x D block held as D x 32 as fp32 rows of D.
+template <int D>
+__device__ __forceinline__ void store_part(float* row, const f32x16_t* acc, int h) {
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = acc[mb][4 * g + i];
+      *reinterpret_cast<f32x4_t*>(row + 32 * mb + 8 * g + 4 * h) = v;
+    }
 }
 
 // Stores a 32 x D block held as D x 32 (column = row of the output), times `mul`.
@@ -190,13 +215,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a);
+  const Place pl = place(a, slots);
   const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
   if (!t.ok) return;
   const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
   const Mask m{Lk - Lq, a.window, a.sinks};
   const int last = Lq - 1;
   const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
+  const Chunks ch = key_chunks(kt.n, a.splits);
+  if (pl.chunk >= ch.n) return;
+  const int it0 = pl.chunk * ch.per, it1 = min(it0 + ch.per, kt.n);
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
   const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
@@ -219,7 +247,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   auto step = [&](int it, const char* __restrict__ K, const char* __restrict__ V, char* __restrict__ nextK,
                   char* __restrict__ nextV) {
     const int j0 = kt.at(it);
-    if (it + 1 < kt.n) {
+    if (it + 1 < it1) {
       fetch(nextK, kb, ks, kt.at(it + 1), Lk - 1, wave);
       fetch(nextV, vb, vs, kt.at(it + 1), Lk - 1, wave);
     }
@@ -271,20 +299,94 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
     }
     tiles_ready();
   };
-  if (kt.n > 0) {
-    fetch(ldsK0, kb, ks, kt.at(0), Lk - 1, wave);
-    fetch(ldsV0, vb, vs, kt.at(0), Lk - 1, wave);
+  if (it0 < it1) {
+    fetch(ldsK0, kb, ks, kt.at(it0), Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(it0), Lk - 1, wave);
   }
   tiles_ready();
-  for (int it = 0; it < kt.n; it += 2) {
+  for (int it = it0; it < it1; it += 2) {
     step(it, ldsK0, ldsV0, ldsK1, ldsV1);
-    if (it + 1 < kt.n) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
+    if (it + 1 < it1) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   sum += __shfl_xor(sum, 32, kWave);
+  if (ch.n > 1) {  // sums [128][D], maxima [128], weights [128] of this chunk
+    float* part = a.part + ((size_t)(pl.chunk * slots + pl.slot) * a.Hq + pl.hq) * attn_fwd_part_floats(D);
+    store_part<D>(part + (size_t)(32 * wave + n) * D, o, h);
+    if (h == 0) {
+      part[(size_t)kAttnQ * D + 32 * wave + n] = mx;
+      part[(size_t)kAttnQ * (D + 1) + 32 * wave + n] = sum;
+    }
+    return;
+  }
   if (r0 + n > last) return;
   store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + pl.hq * a.o.head, o, sum > 0.f ? 1.f / sum : sum, h);
   if (a.lse != nullptr && h == 0)
     a.lse[(size_t)pl.hq * a.Tq + q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+}
+
+// Joins the chunks of the query tiles that were split, in order: a workgroup per 32 rows of a tile and
+// head, eight threads per row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_fwd_join_k(AttnArgs a, int slots) {
+  const int hq = (int)(blockIdx.x % a.Hq), quarter = (int)(blockIdx.x / a.Hq & 3), slot = (int)(blockIdx.x / a.Hq / 4);
+  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, slot);
+  if (!t.ok) return;
+  const Mask m{t.b.n - t.a.n, a.window, a.sinks};
+  const int last = t.a.n - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.b.n);
+  const Chunks ch = key_chunks(kt.n, a.splits);
+  const int row = 32 * quarter + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (D / 8);
+  if (ch.n == 1 || t.row0 + row > last) return;
+  const size_t next = (size_t)slots * a.Hq * attn_fwd_part_floats(D);
+  const float* part = a.part + ((size_t)slot * a.Hq + hq) * attn_fwd_part_floats(D);
+  float mx = -INFINITY, sum = 0.f;
+  f32x4_t o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int kBatch = 4;  // chunks read side by side
+  for (int c0 = 0; c0 < ch.n; c0 += kBatch) {
+    float pm[kBatch], pl[kBatch];
+    f32x4_t x[kBatch][D / 32];
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      const float* p = part + min(c0 + c, ch.n - 1) * next;
+      pm[c] = p[(size_t)kAttnQ * D + row];
+      pl[c] = p[(size_t)kAttnQ * (D + 1) + row];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x[c][i] = *reinterpret_cast<const f32x4_t*>(p + (size_t)row * D + d0 + 4 * i);
+    }
+    float up = mx;
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c)
+      if (c0 + c < ch.n) up = fmaxf(up, pm[c]);
+    const float ref = up > -INFINITY ? up : 0.f, f0 = exp2_hw(mx - ref);
+    mx = up;
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= f0;
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      if (c0 + c >= ch.n) continue;
+      const float f = exp2_hw(pm[c] - ref);
+      sum = fmaf(pl[c], f, sum);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = fmaf(x[c][i][j], f, o[i][j]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum;
+  const long long r = t.a.lo + t.row0 + row;
+  uint16_t* out = a.o.p + r * a.o.token + hq * a.o.head + d0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    uint2 v;
+    v.x = pack_bf16x2(o[i][0] * inv, o[i][1] * inv);
+    v.y = pack_bf16x2(o[i][2] * inv, o[i][3] * inv);
+    *reinterpret_cast<uint2*>(out + 4 * i) = v;
+  }
+  if (a.lse != nullptr && d0 == 0)
+    a.lse[(size_t)hq * a.Tq + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
 }
 
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
@@ -296,13 +398,16 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a);
+  const Place pl = place(a, slots);
   const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
   if (!t.ok) return;
   const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
   const Mask m{Lk - Lq, a.window, a.sinks};
   const int last = Lq - 1;
   const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
+  const Chunks ch = key_chunks(kt.n, b.q_splits);
+  if (pl.chunk >= ch.n) return;
+  const int it0 = pl.chunk * ch.per, it1 = min(it0 + ch.per, kt.n);
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
   const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
@@ -330,7 +435,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
   const size_t stat = (size_t)pl.hq * a.Tq + q0 + r;
   const float lse = a.lse[stat];
   const float lse2 = lse > -INFINITY ? lse * kLog2e : 0.f;  // a row that sees nothing: its scores are all -inf
-  if (h == 0 && r0 + n <= last) {
+  if (pl.chunk == 0 && h == 0 && r0 + n <= last) {
     b.lse2[stat] = lse2;
     b.delta[stat] = delta;
   }
@@ -345,7 +450,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
   auto step = [&](int it, const char* __restrict__ K, const char* __restrict__ V, char* __restrict__ nextK,
                   char* __restrict__ nextV) {
     const int j0 = kt.at(it);
-    if (it + 1 < kt.n) {
+    if (it + 1 < it1) {
       fetch(nextK, kb, ks, kt.at(it + 1), Lk - 1, wave);
       fetch(nextV, vb, vs, kt.at(it + 1), Lk - 1, wave);
     }
@@ -378,17 +483,55 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
     }
     tiles_ready();
   };
-  if (kt.n > 0) {
-    fetch(ldsK0, kb, ks, kt.at(0), Lk - 1, wave);
-    fetch(ldsV0, vb, vs, kt.at(0), Lk - 1, wave);
+  if (it0 < it1) {
+    fetch(ldsK0, kb, ks, kt.at(it0), Lk - 1, wave);
+    fetch(ldsV0, vb, vs, kt.at(it0), Lk - 1, wave);
   }
   tiles_ready();
-  for (int it = 0; it < kt.n; it += 2) {
+  for (int it = it0; it < it1; it += 2) {
     step(it, ldsK0, ldsV0, ldsK1, ldsV1);
-    if (it + 1 < kt.n) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
+    if (it + 1 < it1) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
+  }
+  if (ch.n > 1) {
+    float* part = b.q_part + ((size_t)(pl.chunk * slots + pl.slot) * a.Hq + pl.hq) * kAttnQ * D;
+    store_part<D>(part + (size_t)(32 * wave + n) * D, dq, h);
+    return;
   }
   if (r0 + n <= last)
     store_rows<D>(b.dq.p + (long long)(q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
+}
+
+// Adds the chunks of the query tiles that were split, in order (see attn_fwd_join_k).
+template <int D>
+__global__ __launch_bounds__(256) void attn_dq_join_k(AttnBackwardArgs b, int slots) {
+  const AttnArgs& a = b.f;
+  const int hq = (int)(blockIdx.x % a.Hq), quarter = (int)(blockIdx.x / a.Hq & 3), slot = (int)(blockIdx.x / a.Hq / 4);
+  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, slot);
+  if (!t.ok) return;
+  const Mask m{t.b.n - t.a.n, a.window, a.sinks};
+  const int last = t.a.n - 1;
+  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.b.n);
+  const Chunks ch = key_chunks(kt.n, b.q_splits);
+  const int row = 32 * quarter + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (D / 8);
+  if (ch.n == 1 || t.row0 + row > last) return;
+  const size_t next = (size_t)slots * a.Hq * kAttnQ * D;
+  const float* part = b.q_part + ((size_t)slot * a.Hq + hq) * kAttnQ * D + (size_t)row * D + d0;
+  uint16_t* out = b.dq.p + (long long)(t.a.lo + t.row0 + row) * b.dq.token + hq * b.dq.head + d0;
+  f32x4_t sum[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) sum[i] = *reinterpret_cast<const f32x4_t*>(part + 4 * i);
+#pragma unroll 4
+  for (int c = 1; c < ch.n; ++c)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) sum[i] += *reinterpret_cast<const f32x4_t*>(part + c * next + 4 * i);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const f32x4_t x = sum[i];
+    uint2 v;
+    v.x = pack_bf16x2(x[0] * a.scale, x[1] * a.scale);
+    v.y = pack_bf16x2(x[2] * a.scale, x[3] * a.scale);
+    *reinterpret_cast<uint2*>(out + 4 * i) = v;
+  }
 }
 
 namespace {
@@ -615,19 +758,27 @@ namespace {
 
 template <int D>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
-  const long long slots = attn_slots(a.Tq, a.n_seq, kAttnQ);
-  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq)), dim3(256), 0, s, a, (int)slots);
+  const int slots = (int)attn_slots(a.Tq, a.n_seq, kAttnQ);
+  hipLaunchKernelGGL((attn_fwd_k<D>), dim3((unsigned)(slots * a.Hq * a.splits)), dim3(256), 0, s, a, slots);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((attn_fwd_join_k<D>), dim3((unsigned)(slots * a.Hq * 4)), dim3(256), 0, s, a, slots);
   return hipGetLastError();
 }
 
 template <int D>
 hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
   const AttnArgs& a = b.f;
-  const long long qs = attn_slots(a.Tq, a.n_seq, kAttnQ), ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
+  const long long ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
   if (a.Tq > 0) {
-    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq)), dim3(256), 0, s, b, (int)qs);
-    const hipError_t e = hipGetLastError();
+    const int qs = (int)attn_slots(a.Tq, a.n_seq, kAttnQ);
+    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq * b.q_splits)), dim3(256), 0, s, b, qs);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (b.q_splits > 1) {
+      hipLaunchKernelGGL((attn_dq_join_k<D>), dim3((unsigned)(qs * a.Hq * 4)), dim3(256), 0, s, b, qs);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
   const long long sinks = (long long)b.sink_tiles * a.n_seq;
   hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,

@@ -109,6 +109,10 @@ molora::AttnArgs attn_args(const molora_attn_shape* s, const molora_rows* q, con
   return a;
 }
 
+size_t fwd_bytes_of(const molora_attn_shape* s) {
+  return molora::attn_fwd_ws_bytes(s->Tq, s->Tkv, s->n_seq, s->n_heads, s->head_dim, s->window, s->sinks);
+}
+
 molora::AttnBwdPlan bwd_plan_of(const molora_attn_shape* s) {
   return molora::attn_bwd_plan(s->Tq, s->Tkv, s->n_seq, s->n_heads, s->n_kv_heads, s->head_dim, s->window,
                                s->sinks);
@@ -190,8 +194,16 @@ int molora_route_scores_backward(const float* logits, const int32_t* idx, const 
   return e == hipSuccess ? ok() : hip_fail(e, "route_scores_backward launch");
 }
 
+int molora_attn_forward_workspace(const molora_attn_shape* shape, size_t* bytes) {
+  if (bytes == nullptr) return fail(MOLORA_EINVAL, "bytes is NULL");
+  const int rc = check_shape(shape);
+  if (rc != MOLORA_OK) return rc;
+  *bytes = fwd_bytes_of(shape);
+  return ok();
+}
+
 int molora_attn_forward(const molora_attn_shape* shape, const molora_rows* q, const molora_rows* k,
-                        const molora_rows* v, const molora_rows* o, float* lse, void* stream) {
+                        const molora_rows* v, const molora_rows* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_shape(shape);
   if (rc != MOLORA_OK) return rc;
   const int D = shape->head_dim;
@@ -201,8 +213,13 @@ int molora_attn_forward(const molora_attn_shape* shape, const molora_rows* q, co
   if ((rc = check_rows(o, "o", shape->Tq, shape->n_heads, D, true)) != MOLORA_OK) return rc;
   if (!aligned(lse, 4)) return fail(MOLORA_EINVAL, "lse misaligned");
   if (shape->Tq == 0 || shape->n_seq == 0) return ok();
+  const size_t need = fwd_bytes_of(shape);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
+    return fail(MOLORA_ENOSPC, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need, ws_bytes);
   molora::AttnArgs a = attn_args(shape, q, k, v, o);
   a.lse = lse;
+  a.splits = molora::attn_q_splits(shape->Tq, shape->Tkv, shape->n_seq, shape->n_heads, shape->window, shape->sinks);
+  a.part = static_cast<float*>(ws);
   const hipError_t e = molora::launch_attn_forward(a, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attn_forward launch");
 }
@@ -246,6 +263,8 @@ int molora_attn_backward(const molora_attn_shape* shape, const molora_rows* dout
   b.lse2 = reinterpret_cast<float*>(base + plan.lse_off);
   b.delta = reinterpret_cast<float*>(base + plan.delta_off);
   b.part = reinterpret_cast<float*>(base + plan.part_off);
+  b.q_splits = plan.q_splits;
+  b.q_part = reinterpret_cast<float*>(base + plan.q_part_off);
   b.splits = plan.splits;
   b.sink_splits = plan.sink_splits;
   b.sink_tiles = plan.sink_tiles;

@@ -35,6 +35,8 @@ struct AttnArgs {
   const int32_t* kv_off;
   int n_seq, Hq, Hkv, D, Tq, Tkv, window, sinks;
   float scale;
+  int splits;   // attn_q_splits; the forward's parts in part
+  float* part;  // splits > 1: [splits][query tile slots][Hq] x attn_fwd_part_floats
 };
 hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t s);
 
@@ -43,6 +45,8 @@ struct AttnBackwardArgs {
   Rows dout, dq, dk, dv;
   float* lse2;   // workspace [Hq][Tq]: lse in base 2
   float* delta;  // workspace [Hq][Tq]: rowsum(dO O)
+  int q_splits;   // attn_q_splits
+  float* q_part;  // workspace: the split query tiles' sums
   int splits, sink_splits, sink_tiles, most;  // attn_bwd_plan
   float* part;   // workspace: the split key tiles' sums
 };

@@ -22,6 +22,26 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
   return p;
 }
 
+// Splits: up to kQTarget workgroups, one for each of the 512 places; with half as many the tiles
+// themselves fill the GPU.  A tile cannot be told to be long from here: sequences of kQKeys keys on
+// average are (512 keys gain nothing: 15.8 us whole, 17.1 us split; 1024 keys 24.4 us whole, 18.4 us
+// split).
+int attn_q_splits(int Tq, int Tkv, int n_seq, int n_heads, int window, int sinks) {
+  constexpr long long kQTarget = 512, kQKeys = 768;
+  const long long units = attn_slots(Tq, n_seq, kAttnQ) * n_heads;
+  if (units <= 0 || units >= kQTarget / 2 || Tkv < kQKeys * n_seq) return 1;
+  long long keys = Tkv;
+  if (window > 0) keys = std::min(keys, (long long)window + sinks + 2 * kAttnQ);
+  const long long tiles = (keys + 63) / 64;
+  return (int)std::max(1ll, std::min({kQTarget / units, (tiles + kAttnMinTiles - 1) / kAttnMinTiles, 16ll}));
+}
+
+size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, int window, int sinks) {
+  const int splits = attn_q_splits(Tq, Tkv, n_seq, n_heads, window, sinks);
+  if (splits == 1) return 0;
+  return align256((size_t)splits * attn_slots(Tq, n_seq, kAttnQ) * n_heads * attn_fwd_part_floats(head_dim) * sizeof(float));
+}
+
 // A causal sequence's key tiles are seen by unequal numbers of queries, so with few tiles the longest
 // one sets the time: chunks until there are kBwdTarget workgroups, two for each of the 512 places
 // that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 2127 us unsplit, 1525 us
@@ -59,7 +79,11 @@ AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_head
   p.lse_off = 0;
   p.delta_off = stat;
   p.part_off = 2 * stat;
-  p.total = p.part_off + (size_t)(parts * n_kv_heads * bytes);
+  p.q_splits = attn_q_splits(Tq, Tkv, n_seq, n_heads, window, sinks);
+  p.q_part_off = p.part_off + (size_t)(parts * n_kv_heads * bytes);
+  p.total = p.q_part_off;
+  if (p.q_splits > 1)
+    p.total += align256((size_t)p.q_splits * attn_slots(Tq, n_seq, kAttnQ) * n_heads * kAttnQ * head_dim * sizeof(float));
   return p;
 }
 

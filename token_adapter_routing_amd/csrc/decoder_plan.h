@@ -18,6 +18,13 @@ constexpr int kAttnK = 128;   // key rows per workgroup of the dk / dv pass
 MOLORA_HD inline long long attn_slot0(int off, int s, int tile) { return (long long)(off / tile) + s; }
 MOLORA_HD inline long long attn_slots(int T, int n_seq, int tile) { return (long long)(T / tile) + n_seq; }
 
+// Few query tiles before many keys: the forward and the dq pass split a tile's key tiles over up to
+// attn_q_splits() workgroups, at least kAttnMinTiles of 64 keys each, and join the parts.
+constexpr int kAttnMinTiles = 6;
+int attn_q_splits(int Tq, int Tkv, int n_seq, int n_heads, int window, int sinks);
+MOLORA_HD inline size_t attn_fwd_part_floats(int head_dim) { return (size_t)kAttnQ * (head_dim + 2); }
+size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, int window, int sinks);
+
 // Backward: lse in base 2 and rowsum(dO O), fp32 [heads][Tq] each, then the sums of the key tiles that
 // are split into chunks, [2][kAttnK][head_dim] fp32 per (tile, chunk, kv head): first the sinks' tiles
 // (sink_tiles > 0: that many of every sequence, in sink_splits chunks), then the others (splits > 1).
@@ -26,7 +33,8 @@ constexpr int kAttnMinSteps = 32;  // steps per chunk, at least
 struct AttnBwdPlan {
   int splits, sink_splits, sink_tiles;
   int most;  // steps of the longest tile that is not a sinks' tile
-  size_t lse_off, delta_off, part_off, total;
+  int q_splits;
+  size_t lse_off, delta_off, part_off, q_part_off, total;
 };
 AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks);
 MOLORA_HD inline size_t attn_part_floats(int head_dim) { return (size_t)2 * kAttnK * head_dim; }

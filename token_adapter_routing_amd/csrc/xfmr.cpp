@@ -236,6 +236,7 @@ hipError_t launch_xf_serve(const XfServeLaunch& v, hipStream_t s) {
       t.window = v.window;
       t.sinks = v.sinks;
       t.scale = scale;
+      t.splits = 1;
       XF_HIP(launch_attn_forward(t, s), "attention");
     } else {
       DecodeArgs t{};

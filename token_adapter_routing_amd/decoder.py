@@ -38,7 +38,8 @@ class MoloraKvCache(ctypes.Structure):
 _SIGS = {
     "molora_route_scores": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p, _c_p]),
     "molora_route_scores_backward": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p]),
-    "molora_attn_forward": (_c_i, [_c_p] * 7),
+    "molora_attn_forward_workspace": (_c_i, [_c_p, _c_p]),
+    "molora_attn_forward": (_c_i, [_c_p] * 7 + [_c_sz, _c_p]),
     "molora_attn_backward_workspace": (_c_i, [_c_p, _c_p]),
     "molora_attn_backward": (_c_i, [_c_p] * 11 + [_c_sz, _c_p]),
     "molora_kv_append": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_i, _c_p, _c_p]),
@@ -192,7 +193,8 @@ def _shape(q, k, q_off, kv_off, scale, window, sinks) -> MoloraAttnShape:
 @_on_stream
 def molora_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off: torch.Tensor,
                         kv_off: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
-                        sinks: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+                        sinks: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None):
     """Causal attention of packed sequences: q bf16 [Tq][Hq][D], k and v bf16 [Tkv][Hkv][D] (any token and
     head strides), q_off and kv_off int32 [n_seq + 1] on the GPU; window 0: none.  Returns (o, lse), o
     bf16 [Tq][Hq][D], lse fp32 [Hq][Tq].  scale defaults to 1 / sqrt(D)."""
@@ -203,11 +205,22 @@ def molora_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     if lse is None:
         lse = torch.empty(Hq, Tq, dtype=torch.float32, device=q.device)
     s = _shape(q, k, q_off, kv_off, scale, window, sinks)
-    ref = ctypes.byref
-    _check(_library().molora_attn_forward(
+    lib, ref = _library(), ctypes.byref
+    need = _c_sz()
+    _check(lib.molora_attn_forward_workspace(ref(s), ref(need)))
+    wp, wn, ws = _workspace(ws, need.value, q.device)
+    _check(lib.molora_attn_forward(
         ref(s), ref(_rows(q, (Tq, Hq, D), "q")), ref(_rows(k, kv, "k")), ref(_rows(v, kv, "v")),
-        ref(_rows(out, (Tq, Hq, D), "out")), _flat(lse, torch.float32, (Hq, Tq), "lse"), _stream()))
+        ref(_rows(out, (Tq, Hq, D), "out")), _flat(lse, torch.float32, (Hq, Tq), "lse"), wp, wn, _stream()))
     return out, lse
+
+
+def molora_attn_forward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor, window: int = 0,
+                                  sinks: int = 0) -> int:
+    n = _c_sz()
+    _check(_library().molora_attn_forward_workspace(ctypes.byref(_shape(q, k, q_off, None, None, window, sinks)),
+                                                    ctypes.byref(n)))
+    return n.value
 
 
 def molora_attn_backward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor, window: int = 0,
