@@ -138,6 +138,23 @@ def test_key_tiles_split_into_chunks():
     run(need_gpu(), Case([1600], [1600], 4, 1, 128, window=300, sinks=5, seed=33))
 
 
+def test_sinks_of_many_sequences():
+    """So many sink tiles that they are not taken apart: a long one still runs as a whole."""
+    lens = [400] + [3] * 300 + [700] + [2] * 300
+    run(need_gpu(), Case(lens, lens, 8, 2, 64, window=64, sinks=2, seed=35))
+
+
+def test_no_keys_with_window_and_sinks():
+    m = need_gpu()
+    q = torch.ones(9, 2, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device="cuda")
+    off, none = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    o, lse = m.molora_attn_forward(q, k, k, off, none, window=2, sinks=3)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    dq, dk, dv = m.molora_attn_backward(q, q, k, k, o, lse, off, none, window=2, sinks=3)
+    assert (dq == 0).all() and dk.numel() == 0 and dv.numel() == 0
+
+
 def test_workspace_given():
     m = need_gpu()
     c = Case([20], [1500], 4, 2, 64, seed=34)

@@ -131,6 +131,15 @@ __device__ __forceinline__ bf16x8_t acc_frag(const f32x16_t& v, int s) {
   return as_bf16x8(u);
 }
 
+// What acc_frag rounded away, as bf16 again: together they hold 16 bits of the value.
+__device__ __forceinline__ bf16x8_t acc_rest(const f32x16_t& v, int s, bf16x8_t hi) {
+  u32x4_t u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    u[i] = pack_bf16x2(v[8 * s + 2 * i] - (float)hi[2 * i], v[8 * s + 2 * i + 1] - (float)hi[2 * i + 1]);
+  return as_bf16x8(u);
+}
+
 __device__ __forceinline__ int acc_row(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
 
 // Key tiles a query tile visits: the sinks' first, then the window's.
@@ -391,7 +400,7 @@ __global__ __launch_bounds__(256) void attn_fwd_join_k(AttnArgs a, int slots) {
 
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
 // the keys as the forward does.
-template <int D>
+template <int D, bool FINE>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
@@ -479,6 +488,15 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
           for (int mb = 0; mb < D / 32; ++mb)
             dq[mb] = mfma32x32x16(col_frag<D>(K, lo, 32 * blk + 16 * st, mb), df[st], dq[mb]);
         reads_ahead<D / 16, 1, 2, 4>();
+        if constexpr (FINE) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const bf16x8_t rest = acc_rest(s, st, df[st]);
+#pragma unroll
+            for (int mb = 0; mb < D / 32; ++mb)
+              dq[mb] = mfma32x32x16(col_frag<D>(K, lo, 32 * blk + 16 * st, mb), rest, dq[mb]);
+          }
+        }
       }
     }
     tiles_ready();
@@ -578,6 +596,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
   t.total = t.nt * group;
   const int steps = (t.q.n + kBQ - 1) / kBQ * group, splits = sink ? b.sink_splits : b.splits;
   t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, kAttnMinSteps);
+  t.per = max(t.per, (t.total + splits - 1) / splits);  // never more chunks than there are places
   t.chunks = max((t.total + t.per - 1) / t.per, 1);
   const long long sink_parts = (long long)b.sink_tiles * a.n_seq * b.sink_splits;
   t.part = (sink ? 0 : sink_parts) + (long long)slot * splits;
@@ -590,8 +609,8 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
 // of every query head that reads it (or one chunk of them, whose sums go to the workspace).  S and
 // dP are computed with the queries down, so that P and dS are the right operands of dV^T = dO^T P
 // and dK^T = Q^T dS.
-template <int D>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
+template <int D, bool FINE>
+__global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBQ * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
   __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
@@ -693,6 +712,17 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardA
           dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), df[st], dk[mb]);
         }
       reads_ahead<D / 8, 1, 2, 4>();
+      if constexpr (FINE) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const bf16x8_t pr = acc_rest(s, st, pf[st]), dr = acc_rest(dp, st, df[st]);
+#pragma unroll
+          for (int mb = 0; mb < D / 32; ++mb) {
+            dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pr, dv[mb]);
+            dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), dr, dk[mb]);
+          }
+        }
+      }
     }
     tiles_ready();
   };
@@ -766,13 +796,13 @@ hipError_t forward(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, bool FINE>
 hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
   const AttnArgs& a = b.f;
   const long long ks = attn_slots(a.Tkv, a.n_seq, kAttnK);
   if (a.Tq > 0) {
     const int qs = (int)attn_slots(a.Tq, a.n_seq, kAttnQ);
-    hipLaunchKernelGGL((attn_dq_k<D>), dim3((unsigned)(qs * a.Hq * b.q_splits)), dim3(256), 0, s, b, qs);
+    hipLaunchKernelGGL((attn_dq_k<D, FINE>), dim3((unsigned)(qs * a.Hq * b.q_splits)), dim3(256), 0, s, b, qs);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (b.q_splits > 1) {
@@ -781,7 +811,7 @@ hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
     }
   }
   const long long sinks = (long long)b.sink_tiles * a.n_seq;
-  hipLaunchKernelGGL((attn_dkv_k<D>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,
+  hipLaunchKernelGGL((attn_dkv_k<D, FINE>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,
                      (int)ks);
   const hipError_t e = hipGetLastError();
   const long long joins = sinks + (b.splits > 1 ? ks : 0);
@@ -796,8 +826,14 @@ hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t s) {
   return a.D == 64 ? forward<64>(a, s) : forward<128>(a, s);
 }
 
+// P and dS enter the second products rounded to bf16, which errs as much as the rounding of the result
+// does.  In a batch of few rows single roundings show in the gradients (nothing averages), and the
+// products are a small part of the time: there both go in as a rounded value and its rest (one head of 128,
+// 64 rows: 16.1 us rounded, 17.9 us with the rest).
 hipError_t launch_attn_backward(const AttnBackwardArgs& b, hipStream_t s) {
-  return b.f.D == 64 ? backward<64>(b, s) : backward<128>(b, s);
+  constexpr int kFineRows = 64;
+  if (b.f.Tq <= kFineRows) return b.f.D == 64 ? backward<64, true>(b, s) : backward<128, true>(b, s);
+  return b.f.D == 64 ? backward<64, false>(b, s) : backward<128, false>(b, s);
 }
 
 }  // namespace molora

@@ -64,10 +64,11 @@ AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_head
     if (windowed && sinks > 0) {
       const long long per_seq = (std::min((long long)sinks, (long long)Tkv) + kAttnK - 1) / kAttnK;
       const long long tiles = per_seq * n_seq;
-      const long long n = std::min({2 * kBwdTarget / (tiles * n_kv_heads), 16ll,
-                                    (steps + kAttnMinSteps - 1) / kAttnMinSteps,
-                                    kBwdPartBytes / (tiles * n_kv_heads * bytes)});
-      if (tiles > 0 && n > 1) {
+      const long long n = tiles <= 0 ? 1
+                                     : std::min({2 * kBwdTarget / (tiles * n_kv_heads), 16ll,
+                                                 (steps + kAttnMinSteps - 1) / kAttnMinSteps,
+                                                 kBwdPartBytes / (tiles * n_kv_heads * bytes)});
+      if (n > 1) {
         p.sink_splits = (int)n;
         p.sink_tiles = (int)per_seq;
       }
