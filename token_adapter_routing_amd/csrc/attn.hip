@@ -25,7 +25,6 @@ namespace molora {
 namespace {
 
 constexpr int kBN = 64;  // keys per LDS tile of the forward and the dq pass
-constexpr int kBQ = kAttnStep;  // queries per LDS tile of the dk / dv pass
 
 template <int D>
 struct Tile {
@@ -555,7 +554,7 @@ __global__ __launch_bounds__(256) void attn_dq_join_k(AttnBackwardArgs b, int sl
 namespace {
 
 // A key tile of the dk / dv pass: 128 keys of one key-value head, the queries that see any of them
-// in steps of kBQ rows, taken for every query head that reads the head: `total` steps in `chunks`
+// in steps of attn_step() rows, taken for every query head that reads the head: `total` steps in `chunks`
 // workgroups of `per` steps.  per comes from the longest tile's steps, so that chunks are about
 // equally long and short tiles are not split.
 struct KvTile {
@@ -566,6 +565,7 @@ struct KvTile {
 };
 
 // The tile of place `slot`, or with `sink` set of sinks' tile `slot`.
+template <int kBQ>
 __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool sink, int slots, int slot) {
   const AttnArgs& a = b.f;
   KvTile t{};
@@ -595,7 +595,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
   t.nt = max((i_hi + kBQ - 1) / kBQ - t.t_lo, 0);
   t.total = t.nt * group;
   const int steps = (t.q.n + kBQ - 1) / kBQ * group, splits = sink ? b.sink_splits : b.splits;
-  t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, kAttnMinSteps);
+  t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, 1024 / kBQ);
   t.per = max(t.per, (t.total + splits - 1) / splits);  // never more chunks than there are places
   t.chunks = max((t.total + t.per - 1) / t.per, 1);
   const long long sink_parts = (long long)b.sink_tiles * a.n_seq * b.sink_splits;
@@ -611,7 +611,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
 // and dK^T = Q^T dS.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
-  constexpr int kTileB = kBQ * Tile<D>::kRow;
+  constexpr int kBQ = attn_step(D), kTileB = kBQ * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
   __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
   // The workgroup's V stays in LDS: beside K's operands and the sums of dK and dV in registers it would
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   const bool sink = id < first;
   if (!sink) id -= first;
   const int n_tiles = sink ? sinks : slots, chunk = id / n_tiles;
-  const KvTile t = find_kv_tile(b, sink, slots, id - chunk * n_tiles);
+  const KvTile t = find_kv_tile<attn_step(D)>(b, sink, slots, id - chunk * n_tiles);
   if (!t.ok || chunk >= t.chunks) return;
   const SeqRange qr = t.q, kr = t.k;
   const int k0 = t.k0, Lq = qr.n, Lk = kr.n, nt = t.nt;
@@ -661,27 +661,31 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
     const int hq = hk * group + it / nt, i0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
     fetch(Q, qb + hq * a.q.head, qs, i0, Lq - 1, wave);
     fetch(G, gb + hq * b.dout.head, gs, i0, Lq - 1, wave);
-    if (wave == 0) {
-      const float* src = (lane < kBQ ? b.lse2 : b.delta) + (size_t)hq * a.Tq + qr.lo + min(i0 + (lane & (kBQ - 1)), Lq - 1);
+    if (wave < 2 * kBQ / kWave) {
+      const int at = wave * kWave + lane;
+      const float* src = (at < kBQ ? b.lse2 : b.delta) + (size_t)hq * a.Tq + qr.lo + min(i0 + (at & (kBQ - 1)), Lq - 1);
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)st, 4, 0, 0);
+                                       (__attribute__((address_space(3))) void*)(st + wave * kWave), 4, 0, 0);
     }
   };
   auto step = [&](int it, const char* __restrict__ Q, const char* __restrict__ G, const float* __restrict__ ls,
                   char* __restrict__ nextQ, char* __restrict__ nextG, float* __restrict__ next_st) {
     if (it + 1 < it1) request(it + 1, nextQ, nextG, next_st);
-    const int i0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
+    const int s0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
     LaneOff lo = lo0;
     // opaque: the operands' addresses are made when needed; kept in registers they would spill others
     asm volatile("" : "+v"(lo.row), "+v"(lo.col));
-    const int p_lo = i0 + m.shift, p_hi = min(i0 + kBQ - 1, Lq - 1) + m.shift;
+#pragma unroll
+    for (int sb = kBQ - 32; sb >= 0; sb -= 32) {
+    const int i0 = s0 + sb;
+    const int p_lo = i0 + m.shift, p_hi = min(i0 + 31, Lq - 1) + m.shift;
     if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
-      const bool all = i0 + kBQ <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
+      const bool all = i0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
       f32x16_t s = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
-        s = mfma32x32x16(row_frag<D>(Q, lo, 0, st), kf[st], s);
-        dp = mfma32x32x16(row_frag<D>(G, lo, 0, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
+        s = mfma32x32x16(row_frag<D>(Q, lo, sb, st), kf[st], s);
+        dp = mfma32x32x16(row_frag<D>(G, lo, sb, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
       }
       reads_ahead<D / 16, 2, 3, 3>();
       if (!all) {
@@ -693,8 +697,8 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + 8 * g + 4 * h);
-        const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + 8 * g + 4 * h);
+        const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + sb + 8 * g + 4 * h);
+        const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float pv = exp2_hw(fmaf(s[4 * g + i], c, -l4[i]));
@@ -708,8 +712,8 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int mb = 0; mb < D / 32; ++mb) {
-          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pf[st], dv[mb]);
-          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), df[st], dk[mb]);
+          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pf[st], dv[mb]);
+          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), df[st], dk[mb]);
         }
       reads_ahead<D / 8, 1, 2, 4>();
       if constexpr (FINE) {
@@ -718,11 +722,12 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
           const bf16x8_t pr = acc_rest(s, st, pf[st]), dr = acc_rest(dp, st, df[st]);
 #pragma unroll
           for (int mb = 0; mb < D / 32; ++mb) {
-            dv[mb] = mfma32x32x16(col_frag<D>(G, lo, 16 * st, mb), pr, dv[mb]);
-            dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, 16 * st, mb), dr, dk[mb]);
+            dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pr, dv[mb]);
+            dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), dr, dk[mb]);
           }
         }
       }
+    }
     }
     tiles_ready();
   };
@@ -763,7 +768,7 @@ __global__ __launch_bounds__(256) void attn_dkv_join_k(AttnBackwardArgs b, int s
   const AttnArgs& a = b.f;
   const int hk = (int)(blockIdx.x % a.Hkv), piece = (int)(blockIdx.x / a.Hkv % kJoinParts);
   const int id = (int)(blockIdx.x / a.Hkv / kJoinParts), sinks = b.sink_tiles * a.n_seq;
-  const KvTile t = find_kv_tile(b, id < sinks, slots, id < sinks ? id : id - sinks);
+  const KvTile t = find_kv_tile<attn_step(D)>(b, id < sinks, slots, id < sinks ? id : id - sinks);
   if (!t.ok || t.chunks == 1) return;
   const float* part = b.part + ((size_t)t.part * a.Hkv + hk) * attn_part_floats(D);
   const size_t next = (size_t)a.Hkv * attn_part_floats(D);

@@ -52,21 +52,23 @@ AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_head
   constexpr long long kBwdTarget = 1024, kBwdPartBytes = 512ll << 20;
   AttnBwdPlan p{};
   const long long slots = attn_slots(Tkv, n_seq, kAttnK), units = slots * n_kv_heads, group = n_heads / n_kv_heads;
-  const long long steps = ((long long)Tq + kAttnStep - 1) / kAttnStep * group;
+  const long long rows = attn_step(head_dim), steps = ((long long)Tq + rows - 1) / rows * group;
   const long long bytes = (long long)(attn_part_floats(head_dim) * sizeof(float));
+  const long long min_steps = attn_min_steps(head_dim);
   const bool windowed = window > 0 && window < Tq;
-  p.most = (int)std::min(steps, windowed ? ((long long)window + kAttnK + 2 * kAttnStep - 2) / kAttnStep * group : steps);
+  p.most = (int)std::min(steps, windowed ? ((long long)window + kAttnK + 2 * rows - 2) / rows * group : steps);
   p.splits = p.sink_splits = 1;
   if (units > 0) {
-    p.splits = (int)std::max(1ll, std::min({(kBwdTarget + units - 1) / units, 16ll,
-                                            ((long long)p.most + kAttnMinSteps - 1) / kAttnMinSteps,
+    const long long target = windowed ? kBwdTarget / 2 : kBwdTarget;  // a window's tiles are equally long
+    p.splits = (int)std::max(1ll, std::min({(target + units - 1) / units, 16ll,
+                                            ((long long)p.most + min_steps - 1) / min_steps,
                                             kBwdPartBytes / (units * bytes)}));
     if (windowed && sinks > 0) {
       const long long per_seq = (std::min((long long)sinks, (long long)Tkv) + kAttnK - 1) / kAttnK;
       const long long tiles = per_seq * n_seq;
       const long long n = tiles <= 0 ? 1
                                      : std::min({2 * kBwdTarget / (tiles * n_kv_heads), 16ll,
-                                                 (steps + kAttnMinSteps - 1) / kAttnMinSteps,
+                                                 (steps + min_steps - 1) / min_steps,
                                                  kBwdPartBytes / (tiles * n_kv_heads * bytes)});
       if (n > 1) {
         p.sink_splits = (int)n;

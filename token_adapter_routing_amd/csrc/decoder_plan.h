@@ -28,8 +28,10 @@ size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, 
 // Backward: lse in base 2 and rowsum(dO O), fp32 [heads][Tq] each, then the sums of the key tiles that
 // are split into chunks, [2][kAttnK][head_dim] fp32 per (tile, chunk, kv head): first the sinks' tiles
 // (sink_tiles > 0: that many of every sequence, in sink_splits chunks), then the others (splits > 1).
-constexpr int kAttnStep = 32;      // query rows per step of the dk / dv pass
-constexpr int kAttnMinSteps = 32;  // steps per chunk, at least
+// Query rows per step of the dk / dv pass: with heads of 64 twice as many fit in LDS beside three
+// waves per SIMD, which halves the waits between steps.
+MOLORA_HD constexpr int attn_step(int head_dim) { return head_dim == 64 ? 64 : 32; }
+MOLORA_HD constexpr int attn_min_steps(int head_dim) { return 1024 / attn_step(head_dim); }  // per chunk
 struct AttnBwdPlan {
   int splits, sink_splits, sink_tiles;
   int most;  // steps of the longest tile that is not a sinks' tile
