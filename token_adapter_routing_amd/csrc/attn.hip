@@ -157,6 +157,24 @@ __device__ __forceinline__ KeyTiles key_tiles(const Mask& m, int p_lo, int p_hi,
   return t;
 }
 
+// Scores of one lane's query at position p against keys j0 + acc_row(i, h) of a 32x32 result: -inf
+// where it does not see the key.  Everything is taken relative to the lane's first key, so that each
+// score costs a comparison with a constant or three.
+__device__ __forceinline__ void hide(f32x16_t& s, const Mask& m, int p, int j0, int h) {
+  const int last = p - j0 - 4 * h;
+  if (m.window == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = acc_row(i, 0) <= last ? s[i] : -INFINITY;
+  } else {
+    const int first = last - m.window, sinks = m.sinks - j0 - 4 * h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = acc_row(i, 0);
+      s[i] = r <= last && (r > first || r < sinks) ? s[i] : -INFINITY;
+    }
+  }
+}
+
 // Whether rows at positions [p_lo, p_hi] see nothing, or everything, of keys [j0, j1].
 __device__ __forceinline__ bool sees_none(const Mask& m, int p_lo, int p_hi, int j0, int j1) {
   return j0 > p_hi || (m.window && j1 <= p_lo - m.window && j0 >= m.sinks);
@@ -269,8 +287,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
       if (!sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1)) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[b][i] = m.sees(p, j0 + 32 * b + acc_row(i, h)) ? s[b][i] : -INFINITY;
+          hide(s[b], m, p, j0 + 32 * b, h);
       }
       float top = s[0][0];
 #pragma unroll
@@ -473,10 +490,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
           dp = mfma32x32x16(row_frag<D>(V, lo, 32 * blk, st), g[st], dp);
         }
         reads_ahead<D / 16, 2, 2, 3>();
-        if (!all) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] = m.sees(p, j0 + 32 * blk + acc_row(i, h)) ? s[i] : -INFINITY;
-        }
+        if (!all) hide(s, m, p, j0 + 32 * blk, h);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
         const bf16x8_t df[2] = {acc_frag(s, 0), acc_frag(s, 1)};
@@ -689,11 +703,11 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
       }
       reads_ahead<D / 16, 2, 3, 3>();
       if (!all) {
+        // the queries that see key j: a range of rows, here relative to the lane's first
+        const int first = j - m.shift - i0 - 4 * h, rows = Lq - i0 - 4 * h;
+        const int end = m.window == 0 || j < m.sinks ? rows : min(first + m.window, rows);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int row = i0 + acc_row(i, h);
-          s[i] = row < Lq && m.sees(row + m.shift, j) ? s[i] : -INFINITY;
-        }
+        for (int i = 0; i < 16; ++i) s[i] = acc_row(i, 0) >= first && acc_row(i, 0) < end ? s[i] : -INFINITY;
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {

@@ -117,14 +117,12 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ offa, i
   return t;
 }
 
-// What the queries of one sequence see.
+// What the queries of one sequence see: the query at position p key j when j <= p and (window == 0 or
+// j > p - window or j < sinks).
 struct Mask {
   int shift;   // position of query i: i + shift
   int window;  // 0: none
   int sinks;
-  __device__ __forceinline__ bool sees(int p, int j) const {
-    return j <= p && (window == 0 || j > p - window || j < sinks);
-  }
 };
 
 }  // namespace molora
