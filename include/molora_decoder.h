@@ -52,7 +52,7 @@ enum { MOLORA_SCORE_SOFTMAX = 0, MOLORA_SCORE_SIGMOID = 1 };
  * largest finite number.  A renormalised sum of 0 gives weights 0.
  * Supported: 1 <= K <= 64, 1 <= k <= min(K, 8), n_group divides K,
  * 1 <= topk_group <= n_group, k <= topk_group * K / n_group, N * K < 2^31,
- * factor finite.
+ * N < 2^29, factor finite.
  *
  * molora_route_scores_backward: dL/dlogits with the selection held fixed.
  *   idx     as written by molora_route_scores (entries outside [0, K) receive
@@ -108,7 +108,8 @@ int molora_route_scores_backward(const float *logits, const int32_t *idx, const 
  * are summed in fp32 over their query heads.  Rows outside every sequence are
  * left as they were; rows that nothing sees get 0.
  * Supported: head_dim 64 or 128, 1 <= n_kv_heads, n_heads a multiple of it and
- * at most 1024, n_seq, Tq, Tkv >= 0 and below 2^24, token strides below 2^23,
+ * at most 1024, n_seq, Tq, Tkv >= 0 and below 2^24, (Tq / 128 + n_seq) *
+ * n_heads and (Tkv / 128 + n_seq) * n_kv_heads below 2^24, token strides below 2^23,
  * scale positive and finite, sinks <= 2^24.
  * Errors (nothing enqueued): shapes -> MOLORA_ENOTSUP; NULL or misaligned
  * pointers, bad strides, outputs whose rows overlap, a negative window or
@@ -141,7 +142,8 @@ int molora_attn_backward(const molora_attn_shape *shape, const molora_rows *dout
  * table[b][j / page_size] at row j % page_size.
  *   k, v    device [n_pages][n_kv_heads][page_size][head_dim], bf16 or e4m3
  *   k_scale, v_scale  e4m3: device uint8 [n_pages][n_kv_heads][page_size],
- *           byte e standing for the factor 2^(e - 127) of its row; bf16: NULL
+ *           byte e, 1 <= e <= 254, standing for the factor 2^(e - 127) of its
+ *           row; bf16: NULL
  * Supported: head_dim 64 or 128, page_size 16, 32, 64, 128 or 256.
  *
  * molora_kv_append writes the newest rows of every sequence: the rows

@@ -44,7 +44,7 @@ ROUTE = dict(logits=FAKE, bias=None, N=4, K=16, k=2, score=0, n_group=1, topk_gr
     (dict(n_group=4, topk_group=5), ENOTSUP), (dict(n_group=4, topk_group=0), ENOTSUP),
     (dict(n_group=16, topk_group=1), ENOTSUP), (dict(logits=None), EINVAL), (dict(idx=None), EINVAL),
     (dict(w=None), EINVAL), (dict(logits=FAKE + 4), EINVAL), (dict(idx=FAKE + 2), EINVAL), (dict(bias=FAKE + 1), EINVAL),
-    (dict(N=1 << 30), ENOTSUP)])
+    (dict(N=1 << 30), ENOTSUP), (dict(N=1 << 29, K=1, k=1), ENOTSUP)])
 def test_route_scores_refusals(change, code):
     a = dict(ROUTE, **change)
     assert lib().molora_route_scores(*a.values()) == code, last()
@@ -86,7 +86,8 @@ def attn(s=None, q=None, k=None, v=None, o=None, lse=FAKE, ws=None, size=0):
 @pytest.mark.parametrize("change,code", [
     (dict(head_dim=96), ENOTSUP), (dict(head_dim=0), ENOTSUP), (dict(n_kv_heads=0), ENOTSUP), (dict(n_kv_heads=3), ENOTSUP),
     (dict(n_heads=0), ENOTSUP), (dict(n_heads=2048), ENOTSUP), (dict(n_seq=-1), EINVAL), (dict(Tq=-1), EINVAL),
-    (dict(Tkv=-1), EINVAL), (dict(Tq=1 << 24), ENOTSUP), (dict(n_seq=(1 << 24) - 1, n_heads=1024), ENOTSUP),
+    (dict(Tkv=-1), EINVAL), (dict(Tq=1 << 24), ENOTSUP), (dict(Tq=1 << 23, n_heads=1024), ENOTSUP),
+    (dict(n_seq=1 << 21), ENOTSUP), (dict(n_seq=(1 << 24) - 1, n_heads=1024), ENOTSUP),
     (dict(window=-1), EINVAL), (dict(sinks=-1), EINVAL), (dict(sinks=(1 << 24) + 1), ENOTSUP), (dict(scale=0.0), EINVAL),
     (dict(scale=-1.0), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
     (dict(q_off=None), EINVAL), (dict(q_off=FAKE + 2), EINVAL), (dict(kv_off=FAKE + 1), EINVAL)])

@@ -21,6 +21,7 @@ static_assert(MOLORA_SCORE_SOFTMAX == molora::kScoreSoftmax && MOLORA_SCORE_SIGM
 namespace {
 
 constexpr long long kMaxRows = 1ll << 24;      // tokens, sequences
+constexpr long long kMaxGroups = 1ll << 24;    // workgroups of a launch: 2^32 threads of 256 each
 constexpr long long kMaxStride = 1ll << 23;    // elements between tokens: 64 rows fit 32-bit byte offsets
 constexpr int kMaxWindow = 1 << 25;            // wider than any sequence
 
@@ -52,7 +53,8 @@ int check_score(int N, int K, int k, int score, float factor) {
   if (K < 1 || K > MOLORA_MAX_ADAPTERS) return fail(MOLORA_ENOTSUP, "K=%d outside [1, %d]", K, MOLORA_MAX_ADAPTERS);
   if (k < 1 || k > K || k > MOLORA_MAX_TOPK)
     return fail(MOLORA_ENOTSUP, "k=%d outside [1, min(K=%d, %d)]", k, K, MOLORA_MAX_TOPK);
-  if ((long long)N * K >= (1ll << 31)) return fail(MOLORA_ENOTSUP, "N*K=%lld too large", (long long)N * K);
+  if ((long long)N * K >= (1ll << 31) || N >= (1 << 29))
+    return fail(MOLORA_ENOTSUP, "N=%d tokens of K=%d logits: too many", N, K);
   if (score != MOLORA_SCORE_SOFTMAX && score != MOLORA_SCORE_SIGMOID) return fail(MOLORA_EINVAL, "score=%d", score);
   if (!std::isfinite(factor)) return fail(MOLORA_EINVAL, "factor is not finite");
   return MOLORA_OK;
@@ -80,7 +82,7 @@ int check_shape(const molora_attn_shape* s) {
   if (s->n_seq >= kMaxRows || s->Tq >= kMaxRows || s->Tkv >= kMaxRows)
     return fail(MOLORA_ENOTSUP, "n_seq=%d, Tq=%d, Tkv=%d too large", s->n_seq, s->Tq, s->Tkv);
   if (std::max(molora::attn_slots(s->Tq, s->n_seq, molora::kAttnQ) * s->n_heads,
-               molora::attn_slots(s->Tkv, s->n_seq, molora::kAttnK) * s->n_kv_heads * 32) >= (1ll << 31))
+               molora::attn_slots(s->Tkv, s->n_seq, molora::kAttnK) * s->n_kv_heads) >= kMaxGroups)
     return fail(MOLORA_ENOTSUP, "too many (tile, head) pairs");
   if ((rc = check_mask(s->window, s->sinks, s->scale)) != MOLORA_OK) return rc;
   if (s->n_seq > 0 && (s->q_off == nullptr || !aligned(s->q_off, 4) || !aligned(s->kv_off, 4)))
@@ -356,7 +358,7 @@ static int check_serve(int d, int f, int n_layers, const molora_xf_layer* layers
   if (n_seq < 0 || N < 0) return fail(MOLORA_EINVAL, "n_seq=%d, N=%d", n_seq, N);
   const int heads = d / molora::kXfHeadDim;
   if (N >= kMaxRows || (long long)N * std::max(d, f) >= (1ll << 31) || heads > 1024 ||
-      (long long)n_seq * heads >= kMaxRows || molora::attn_slots(N, n_seq, molora::kAttnQ) * heads >= (1ll << 31))
+      (long long)n_seq * heads >= kMaxRows || molora::attn_slots(N, n_seq, molora::kAttnQ) * heads >= kMaxGroups)
     return fail(MOLORA_ENOTSUP, "batch of %d tokens in %d sequences too large", N, n_seq);
   if (k < 1 || k > MOLORA_MAX_TOPK) return fail(MOLORA_ENOTSUP, "k=%d outside [1, %d]", k, MOLORA_MAX_TOPK);
   for (int l = 0; l < n_layers; ++l) {

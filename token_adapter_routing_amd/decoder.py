@@ -9,6 +9,7 @@ torch, nothing is computed here.  Tensors have to be on the current device.  Wor
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -129,8 +130,8 @@ def _stream() -> int:
     return _raw_stream(_current_device()) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device) -> Tuple[Optional[int], int]:
-    """Pointer and size of the caller's workspace (uint8, checked by the library) or of a new one."""
+def _workspace(ws: Optional[torch.Tensor], need: int, device):
+    """Pointer and size of the caller's workspace (uint8, checked by the library) or of a new one, and it."""
     if ws is None:
         if need == 0:
             return None, 0, None
@@ -179,6 +180,25 @@ def molora_route_scores_backward(logits: torch.Tensor, idx: torch.Tensor, dw: to
 
 # ----------------------------------------------------------------------------------- attention
 
+@functools.lru_cache(maxsize=256)
+def _attn_bytes(backward: bool, n_seq: int, Hq: int, Hkv: int, D: int, Tq: int, Tkv: int, window: int, sinks: int) -> int:
+    """A call's workspace, which goes by these numbers alone (the address stands for offsets)."""
+    lib, n = _library(), _c_sz()
+    fn = lib.molora_attn_backward_workspace if backward else lib.molora_attn_forward_workspace
+    _check(fn(ctypes.byref(MoloraAttnShape(n_seq, Hq, Hkv, D, Tq, Tkv, 256, None, window, sinks, 1.0)),
+              ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(n_pages: int, heads: int, page: int, D: int, n_seq: int, n_heads: int, width: int) -> int:
+    n = _c_sz()
+    _check(_library().molora_attn_decode_workspace(
+        ctypes.byref(MoloraKvCache(None, None, None, None, n_pages, heads, page, D, BF16)), n_seq, n_heads, width,
+        ctypes.byref(n)))
+    return n.value
+
+
 def _shape(q, k, q_off, kv_off, scale, window, sinks) -> MoloraAttnShape:
     Tq, Hq, D = q.shape
     Tkv, Hkv, _ = k.shape
@@ -206,9 +226,7 @@ def molora_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
         lse = torch.empty(Hq, Tq, dtype=torch.float32, device=q.device)
     s = _shape(q, k, q_off, kv_off, scale, window, sinks)
     lib, ref = _library(), ctypes.byref
-    need = _c_sz()
-    _check(lib.molora_attn_forward_workspace(ref(s), ref(need)))
-    wp, wn, ws = _workspace(ws, need.value, q.device)
+    wp, wn, ws = _workspace(ws, _attn_bytes(False, s.n_seq, Hq, kv[1], D, Tq, kv[0], s.window, s.sinks), q.device)
     _check(lib.molora_attn_forward(
         ref(s), ref(_rows(q, (Tq, Hq, D), "q")), ref(_rows(k, kv, "k")), ref(_rows(v, kv, "v")),
         ref(_rows(out, (Tq, Hq, D), "out")), _flat(lse, torch.float32, (Hq, Tq), "lse"), wp, wn, _stream()))
@@ -217,18 +235,16 @@ def molora_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
 
 def molora_attn_forward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor, window: int = 0,
                                   sinks: int = 0) -> int:
-    n = _c_sz()
-    _check(_library().molora_attn_forward_workspace(ctypes.byref(_shape(q, k, q_off, None, None, window, sinks)),
-                                                    ctypes.byref(n)))
-    return n.value
+    """Bytes of molora_attn_forward's ``ws`` for these shapes."""
+    return _attn_bytes(False, q_off.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], int(window),
+                       int(sinks))
 
 
 def molora_attn_backward_workspace(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor, window: int = 0,
                                    sinks: int = 0) -> int:
-    n = _c_sz()
-    _check(_library().molora_attn_backward_workspace(ctypes.byref(_shape(q, k, q_off, None, None, window, sinks)),
-                                                     ctypes.byref(n)))
-    return n.value
+    """Bytes of molora_attn_backward's ``ws`` for these shapes."""
+    return _attn_bytes(True, q_off.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], int(window),
+                       int(sinks))
 
 
 @_on_stream
@@ -248,9 +264,7 @@ def molora_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
         dv = torch.empty(kv, dtype=torch.bfloat16, device=q.device)
     s = _shape(q, k, q_off, kv_off, scale, window, sinks)
     lib, ref = _library(), ctypes.byref
-    need = _c_sz()
-    _check(lib.molora_attn_backward_workspace(ref(s), ref(need)))
-    wp, wn, ws = _workspace(ws, need.value, q.device)
+    wp, wn, ws = _workspace(ws, _attn_bytes(True, s.n_seq, Hq, kv[1], D, Tq, kv[0], s.window, s.sinks), q.device)
     _check(lib.molora_attn_backward(
         ref(s), ref(_rows(dout, qs, "dout")), ref(_rows(q, qs, "q")), ref(_rows(k, kv, "k")), ref(_rows(v, kv, "v")),
         ref(_rows(o, qs, "o")), _flat(lse, torch.float32, (Hq, Tq), "lse"), ref(_rows(dq, qs, "dq")),
@@ -300,6 +314,7 @@ def molora_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, q_off: Op
     """Writes the newest rows of every sequence: rows [q_off[b], q_off[b+1]) of k and v (bf16 [T][Hkv][D])
     become the last ones of lens[b] tokens; q_off None: one row per sequence.  table int32
     [n_seq][width], lens int32 [n_seq], on the GPU."""
+    _here(cache.k, "cache")
     n, width = table.shape
     shape = (k.shape[0], cache.n_kv_heads, cache.head_dim)
     ref = ctypes.byref
@@ -310,9 +325,9 @@ def molora_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, q_off: Op
 
 
 def molora_attn_decode_workspace(cache: KvCache, n_seq: int, n_heads: int, table_width: int) -> int:
-    n = _c_sz()
-    _check(_library().molora_attn_decode_workspace(cache._ref, int(n_seq), int(n_heads), int(table_width), ctypes.byref(n)))
-    return n.value
+    """Bytes of molora_attn_decode's ``ws``."""
+    return _decode_bytes(cache.n_pages, cache.n_kv_heads, cache.page_size, cache.head_dim, int(n_seq), int(n_heads),
+                         int(table_width))
 
 
 @_on_stream
@@ -322,6 +337,7 @@ def molora_attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, len
                        ws: Optional[torch.Tensor] = None):
     """Attention of one new token per sequence over the cache: q bf16 [n_seq][Hq][D], table int32
     [n_seq][width], lens int32 [n_seq] (with the new token).  Returns (o, lse), lse fp32 [n_seq][Hq]."""
+    _here(cache.k, "cache")
     n, Hq, D = q.shape
     width = table.shape[1]
     if out is None:
@@ -329,9 +345,7 @@ def molora_attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, len
     if lse is None:
         lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
     lib, ref = _library(), ctypes.byref
-    need = _c_sz()
-    _check(lib.molora_attn_decode_workspace(cache._ref, n, Hq, width, ref(need)))
-    wp, wn, ws = _workspace(ws, need.value, q.device)
+    wp, wn, ws = _workspace(ws, molora_attn_decode_workspace(cache, n, Hq, width), q.device)
     qs = (n, Hq, cache.head_dim)
     _check(lib.molora_attn_decode(
         cache._ref, ref(_rows(q, qs, "q")), ref(_rows(out, qs, "out")), _flat(lse, torch.float32, (n, Hq), "lse"), n, Hq,
@@ -345,6 +359,8 @@ def molora_attn_decode(q: torch.Tensor, cache: KvCache, table: torch.Tensor, len
 def _caches(model, caches):
     if len(caches) != len(model.layers):
         raise ValueError(f"{len(model.layers)} layers need as many caches, got {len(caches)}")
+    for c in caches:
+        _here(c.k, "cache")
     return (MoloraKvCache * len(caches))(*[c._c for c in caches])
 
 
