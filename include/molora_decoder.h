@@ -92,8 +92,8 @@ int molora_route_scores_backward(const float *logits, const int32_t *idx, const 
  *   window  0: none (sinks has no effect); else at least 1
  * Rows of o and entries of lse outside every sequence are left as they were,
  * and rows of q, k and v outside every sequence are not read into any result.
- * Inside a sequence k and v have to be finite: a NaN or an infinity in row j
- * may reach any output row of its sequence.
+ * Infinities and NaN reach the results of the pairs that see them and no
+ * others (rows of sums that share a tile with one are taken again, more slowly).
  * Products are bf16 with fp32 accumulation; the softmax runs in fp32 and its
  * weights enter the second product as bf16; o is rounded once at the store.
  * Where few query rows face many keys the keys are split over workgroups and

@@ -357,6 +357,61 @@ def test_gradients_against_differences():
         assert abs(want - have) <= 4 * 2.0 ** -7 * np.linalg.norm(f64(got[i]) * d)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,kv_lens,window,sinks,keys,queries", [
+    ([200], [200], 0, 0, [150, 199], [60]),          # later tokens
+    ([300], [300], 40, 3, [100, 170], [5, 220]),     # behind the window, between sinks and window
+    ([150, 90], [150, 95], 33, 0, [0, 149, 200], [149]),
+    ([24], [1500], 300, 20, [600, 1490], [3]),       # keys split over workgroups
+    ([1700], [1700], 200, 5, [900, 1301], [777]),    # key tiles split into chunks
+    ([60], [20], 5, 0, [19], [10, 59]),              # a bad row that sees nothing
+])
+def test_rows_that_are_not_finite_reach_only_what_sees_them(lens, kv_lens, window, sinks, keys, queries, D):
+    """NaN and infinities in tokens: whatever does not see them is as if they were not there."""
+    m = need_gpu()
+    c = Case(lens, kv_lens, 4, 2, D, window=window, sinks=sinks, seed=40)
+    for x, rows in ((c.k, keys), (c.v, keys), (c.q, queries), (c.do, queries)):
+        x[rows] = 0
+    ref = c.oracle()
+    q, k, v, do = (x.cuda() for x in (c.q, c.k, c.v, c.do))
+    for i, j in enumerate(keys):  # in turn: only the key, only one value, both
+        if i != 1:
+            k[j] = float("nan")
+        if i != 0:
+            v[j, :, 3] = float("inf")
+            v[j, :, 40:] = float("nan")
+    for i, j in enumerate(queries):
+        if i != 0:
+            q[j] = float("nan")
+        do[j, :, 7:] = float("-inf")
+    q_off, kv_off = c.off()
+    o, lse = m.molora_attn_forward(q, k, v, q_off, kv_off, **c.kw)
+    see = np.zeros((c.q.shape[0], c.k.shape[0]), bool)
+    for (a, b), (s, e) in zip(zip(c.q_off, c.q_off[1:]), zip(c.kv_off, c.kv_off[1:])):
+        see[a:b, s:e] = O.visible(b - a, e - s, window, sinks)
+    lost = see[:, keys].any(1)          # rows of o
+    lost[queries[1:]] |= see[queries[1:]].any(1)
+    held = o.cpu()
+    assert not torch.isfinite(held[lost]).all(-1).any()
+    held[lost], lse_h = torch.from_numpy(ref[0][lost]).to(torch.bfloat16), lse.cpu()
+    lse_h[:, lost] = torch.from_numpy(ref[1][:, lost]).float()
+    check_forward(c, held, lse_h)
+    got = m.molora_attn_backward(do, q, k, v, o, lse, q_off, kv_off, **c.kw)
+    s = 1 / math.sqrt(D)
+    want, mag, wide = O.attn_backward(f64(c.do), f64(c.q), f64(c.k), f64(c.v), f64(held), f64(lse_h), c.q_off, c.kv_off, s,
+                                      **c.kw)
+    bad = lost.copy()
+    bad[queries] |= see[queries].any(1)
+    gone = see[bad].any(0)              # keys that a bad row sees
+    assert (~bad).any()
+    for name, g, r, a, w, out in zip(("dq", "dk", "dv"), got, want, mag, wide, (bad, gone, gone)):
+        g = f64(g)
+        if name != "dv":                  # (P dO may be finite where dS is not)
+            assert not np.isfinite(g[out]).all(-1).any(), name
+        err, bound = np.abs(g - r)[~out], (HALF * (a + np.abs(r)) + FINE * w + 1e-30)[~out]
+        assert (err <= bound).all(), (name, int((~(err <= bound)).sum()))
+
+
 def test_repeats_are_equal_bit_for_bit():
     m = need_gpu()
     c = Case([400, 77], [400, 77], 8, 2, 128, window=90, sinks=4, seed=19)

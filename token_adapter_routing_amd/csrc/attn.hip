@@ -183,14 +183,104 @@ __device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int 
   return j1 <= p_lo && (!m.window || j0 > p_hi - m.window || j1 < m.sinks);
 }
 
+// ---- Rows taken again.  A hidden pair has weight 0, but 0 times an infinity or a NaN is NaN, so a row of
+// sums that is not finite may owe it to a row that it does not see and that shares a tile with one
+// that it does.  Such rows are summed again over the visible pairs alone, a lane per pair for the
+// weights and then a lane per column.  Finite inputs never come here; the test itself is within the
+// spread of the measurements (train batch 270 us without it, 268 us with it).
+
+// The workgroup's number and the kernel's first argument, read afresh where rows are taken again:
+// otherwise all they lead to would be kept in scalar registers, and spilled, while the products run (8192
+// tokens, 32 / 8 heads of 128: dq and dk / dv 780 + 1254 us with it kept, 740 + 1144 us read afresh).
+__device__ __forceinline__ unsigned group_again() {
+  unsigned id = blockIdx.x;
+  asm volatile("" : "+s"(id));
+  return id;
+}
+template <typename Args>
+__device__ __forceinline__ const Args& args_again() {
+  auto p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Args*)(const void*)p;
+}
+
+// Rows of a 32 x D block held as D x 32 that are not finite (bit per row).
+template <int D>
+__device__ __forceinline__ uint32_t odd_rows(const f32x16_t* acc, bool mine) {
+  float zero[D / 32];  // 0 times a finite value; NaN otherwise
+#pragma unroll
+  for (int mb = 0; mb < D / 32; ++mb) {
+    zero[mb] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero[mb] = fmaf(acc[mb][i], 0.f, zero[mb]);
+  }
+#pragma unroll
+  for (int mb = 1; mb < D / 32; ++mb) zero[0] += zero[mb];
+  const uint64_t b = __ballot(mine && zero[0] != zero[0]);
+  return (uint32_t)(b | (b >> 32));
+}
+
+__device__ __forceinline__ bool sees(const Mask& m, int p, int j) {
+  return j <= p && (!m.window || j > p - m.window || j < m.sinks);
+}
+
+template <int D>
+__device__ __forceinline__ float dot_rows(const uint16_t* x, const uint16_t* y) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < D; i += 8) {
+    const u32x4_t u = ld16(x + i), v = ld16(y + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(bf16_to_f32(u[e] & 0xffffu), bf16_to_f32(v[e] & 0xffffu), s);
+      s = fmaf(bf16_to_f32(u[e] >> 16), bf16_to_f32(v[e] >> 16), s);
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ float lane_value(float v, int i) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+}
+
+// One row of sums, D / 64 columns per lane.
+template <int D>
+struct RowSum {
+  float x[D / 64] = {};
+  // Adds w times row i of `base` for every lane i of `who`.
+  __device__ __forceinline__ void add(uint64_t who, float w, const uint16_t* base, long long stride, int lane) {
+    for (; who; who &= who - 1) {
+      const int i = __builtin_ctzll(who);
+      const float f = lane_value(w, i);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) x[c] = fmaf(f, bf16_to_f32(base[i * stride + D / 64 * lane + c]), x[c]);
+    }
+  }
+  // Nothing that is added can change it.
+  __device__ __forceinline__ bool lost() const {
+    bool nan = true;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) nan &= x[c] != x[c];
+    return __all(nan);
+  }
+  __device__ __forceinline__ void store(uint16_t* row, float mul, int lane) const {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) row[D / 64 * lane + c] = (uint16_t)pack_bf16x2(x[c] * mul, 0.f);
+  }
+  __device__ __forceinline__ void store_part(float* row, int lane) const {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) row[D / 64 * lane + c] = x[c];
+  }
+};
+
 // Workgroup -> (head, slot, chunk of the slot's key tiles): the heads of one key-value head follow each
 // other on one XCD (consecutive workgroups go round the XCDs); the chunk is the slowest, so that
 // workgroups without work lie together at the end.
 struct Place {
   int hq, hk, slot, chunk;
 };
-__device__ __forceinline__ Place place(const AttnArgs& a, int slots) {
-  const unsigned g = a.Hq / a.Hkv, id = blockIdx.x, rest = id / a.Hkv, hk = id % a.Hkv, at = rest / g;
+__device__ __forceinline__ Place place(const AttnArgs& a, int slots, unsigned id) {
+  const unsigned g = a.Hq / a.Hkv, rest = id / a.Hkv, hk = id % a.Hkv, at = rest / g;
   const unsigned chunk = at / slots;
   return {(int)(hk * g + rest % g), (int)hk, (int)(at - chunk * slots), (int)chunk};
 }
@@ -202,6 +292,31 @@ struct Chunks {
 __device__ __forceinline__ Chunks key_chunks(int tiles, int splits) {
   const int per = max((tiles + splits - 1) / splits, kAttnMinTiles);
   return {per, max((tiles + per - 1) / per, 1)};
+}
+
+// A workgroup's query tile and its chunk of the key tiles.
+struct QTile {
+  Mask m;
+  KeyTiles kt;
+  int hq, hk, slot, chunk, chunks, it0, it1;
+  int q0, k0, Lk, last, row0;  // first rows of the sequence, keys, last query, tile's first query
+  bool ok;
+};
+__device__ __forceinline__ QTile q_tile(const AttnArgs& a, int slots, unsigned id, int splits) {
+  QTile x{};
+  const Place pl = place(a, slots, id);
+  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
+  if (!t.ok) return x;
+  x.hq = pl.hq, x.hk = pl.hk, x.slot = pl.slot, x.chunk = pl.chunk;
+  x.q0 = t.a.lo, x.k0 = t.b.lo, x.Lk = t.b.n, x.last = t.a.n - 1, x.row0 = t.row0;
+  x.m = Mask{x.Lk - t.a.n, a.window, a.sinks};
+  x.kt = key_tiles(x.m, x.row0 + x.m.shift, min(x.row0 + kAttnQ - 1, x.last) + x.m.shift, x.Lk);
+  const Chunks ch = key_chunks(x.kt.n, splits);
+  x.chunks = ch.n;
+  x.it0 = x.chunk * ch.per;
+  x.it1 = min(x.it0 + ch.per, x.kt.n);
+  x.ok = x.chunk < ch.n;
+  return x;
 }
 
 // Stores a 32 x D block held as D x 32 as fp32 rows of D.
@@ -234,6 +349,38 @@ __device__ __forceinline__ void store_rows(uint16_t* row, const f32x16_t* acc, f
 
 }  // namespace
 
+namespace {
+
+// attn_fwd_k's rows that are taken again: the wave's rows of the bits of `again`, with the reference
+// maxima and the sums' inverses that the lanes hold.
+template <int D>
+__device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t again, int wave, int lane, float mx,
+                                          float inv) {
+  const QTile t = q_tile(a, slots, group_again(), a.splits);
+  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + t.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + t.hk * a.v.head;
+  const float c = a.scale * kLog2e;
+  for (uint32_t left = again; left; left &= left - 1) {
+    const int i = __builtin_ctz(left), at = 32 * wave + i, p = t.row0 + at + t.m.shift;
+    const long long row = t.q0 + t.row0 + at;
+    const uint16_t* qr = a.q.p + row * a.q.token + t.hq * a.q.head;
+    const float top = lane_value(mx, i), ref = top > -INFINITY ? top : 0.f;
+    RowSum<D> x;
+    for (int it = t.it0; it < t.it1 && !x.lost(); ++it) {
+      const int j0 = t.kt.at(it), j = j0 + lane;
+      const bool see = sees(t.m, p, j);
+      const float w = see ? exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -ref)) : 0.f;
+      x.add(__ballot(see), w, vb + j0 * a.v.token, a.v.token, lane);
+    }
+    if (t.chunks > 1)
+      x.store_part(a.part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * attn_fwd_part_floats(D) + (size_t)at * D,
+                   lane);
+    else x.store(a.o.p + row * a.o.token + t.hq * a.o.head, lane_value(inv, i), lane);
+  }
+}
+
+}  // namespace
+
 // A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
@@ -241,23 +388,19 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a, slots);
-  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
+  const QTile t = q_tile(a, slots, blockIdx.x, a.splits);
   if (!t.ok) return;
-  const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
-  const Mask m{Lk - Lq, a.window, a.sinks};
-  const int last = Lq - 1;
-  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
-  const Chunks ch = key_chunks(kt.n, a.splits);
-  if (pl.chunk >= ch.n) return;
-  const int it0 = pl.chunk * ch.per, it1 = min(it0 + ch.per, kt.n);
+  const Mask m = t.m;
+  const KeyTiles kt = t.kt;
+  const int Lk = t.Lk, q0 = t.q0, k0 = t.k0, last = t.last;
+  const int it0 = t.it0, it1 = t.it1;
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
-  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
-  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + pl.hk * a.v.head;
+  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + t.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + t.hk * a.v.head;
   bf16x8_t q[D / 16];
   {
-    const uint16_t* qr = a.q.p + (long long)(q0 + r) * a.q.token + pl.hq * a.q.head + 8 * h;
+    const uint16_t* qr = a.q.p + (long long)(q0 + r) * a.q.token + t.hq * a.q.head + 8 * h;
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) q[st] = as_bf16x8(ld16(qr + 16 * st));
   }
@@ -334,19 +477,23 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
     if (it + 1 < it1) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   sum += __shfl_xor(sum, 32, kWave);
-  if (ch.n > 1) {  // sums [128][D], maxima [128], weights [128] of this chunk
-    float* part = a.part + ((size_t)(pl.chunk * slots + pl.slot) * a.Hq + pl.hq) * attn_fwd_part_floats(D);
-    store_part<D>(part + (size_t)(32 * wave + n) * D, o, h);
+  const bool mine = r0 + n <= last;
+  const uint32_t again = odd_rows<D>(o, mine && sum < INFINITY);
+  const bool whole = mine && !(again >> n & 1);
+  const float inv = sum > 0.f ? 1.f / sum : sum;
+  if (t.chunks > 1) {  // sums [128][D], maxima [128], weights [128] of this chunk
+    float* part = a.part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * attn_fwd_part_floats(D);
+    if (whole) store_part<D>(part + (size_t)(32 * wave + n) * D, o, h);
     if (h == 0) {
       part[(size_t)kAttnQ * D + 32 * wave + n] = mx;
       part[(size_t)kAttnQ * (D + 1) + 32 * wave + n] = sum;
     }
-    return;
+  } else {
+    if (whole) store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + t.hq * a.o.head, o, inv, h);
+    if (mine && a.lse != nullptr && h == 0)
+      a.lse[(size_t)t.hq * a.Tq + q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
   }
-  if (r0 + n > last) return;
-  store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + pl.hq * a.o.head, o, sum > 0.f ? 1.f / sum : sum, h);
-  if (a.lse != nullptr && h == 0)
-    a.lse[(size_t)pl.hq * a.Tq + q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+  if (again) fwd_again<D>(args_again<AttnArgs>(), slots, again, wave, lane, mx, inv);
 }
 
 // Joins the chunks of the query tiles that were split, in order: a workgroup per 32 rows of a tile and
@@ -414,36 +561,68 @@ __global__ __launch_bounds__(256) void attn_fwd_join_k(AttnArgs a, int slots) {
     a.lse[(size_t)hq * a.Tq + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
 }
 
+namespace {
+
+// attn_dq_k's rows that are taken again (see fwd_again).
+template <int D>
+__device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, uint32_t again, int wave, int lane, float lse2,
+                                         float delta) {
+  const AttnArgs& a = b.f;
+  const QTile t = q_tile(a, slots, group_again(), b.q_splits);
+  const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + t.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + t.hk * a.v.head;
+  const float c = a.scale * kLog2e;
+  for (uint32_t left = again; left; left &= left - 1) {
+    const int i = __builtin_ctz(left), at = 32 * wave + i, p = t.row0 + at + t.m.shift;
+    const long long row = t.q0 + t.row0 + at;
+    const uint16_t* qr = a.q.p + row * a.q.token + t.hq * a.q.head;
+    const uint16_t* gr = b.dout.p + row * b.dout.token + t.hq * b.dout.head;
+    const float li = lane_value(lse2, i), di = lane_value(delta, i);
+    RowSum<D> x;
+    for (int it = t.it0; it < t.it1 && !x.lost(); ++it) {
+      const int j0 = t.kt.at(it), j = j0 + lane;
+      const bool see = sees(t.m, p, j);
+      float w = 0.f;
+      if (see) {
+        w = exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -li));
+        w *= dot_rows<D>(gr, vb + j * a.v.token) - di;
+      }
+      x.add(__ballot(see), w, kb + j0 * a.k.token, a.k.token, lane);
+    }
+    if (t.chunks > 1)
+      x.store_part(b.q_part + (((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * kAttnQ + at) * D, lane);
+    else x.store(b.dq.p + row * b.dq.token + t.hq * b.dq.head, a.scale, lane);
+  }
+}
+
+}  // namespace
+
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
 // the keys as the forward does.
 template <int D, bool FINE>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
-  const Place pl = place(a, slots);
-  const SeqTile t = find_tile<true, true, kAttnQ>(a.q_off, a.Tq, a.kv_off, a.Tkv, a.n_seq, slots, pl.slot);
+  const QTile t = q_tile(a, slots, blockIdx.x, b.q_splits);
   if (!t.ok) return;
-  const int Lq = t.a.n, Lk = t.b.n, q0 = t.a.lo, k0 = t.b.lo;
-  const Mask m{Lk - Lq, a.window, a.sinks};
-  const int last = Lq - 1;
-  const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, Lk);
-  const Chunks ch = key_chunks(kt.n, b.q_splits);
-  if (pl.chunk >= ch.n) return;
-  const int it0 = pl.chunk * ch.per, it1 = min(it0 + ch.per, kt.n);
+  const Mask m = t.m;
+  const KeyTiles kt = t.kt;
+  const int Lk = t.Lk, q0 = t.q0, k0 = t.k0, last = t.last;
+  const int it0 = t.it0, it1 = t.it1;
   const int r0 = t.row0 + 32 * wave, r = min(r0 + n, last);
   const int p = r + m.shift, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
-  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + pl.hk * a.k.head;
-  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + pl.hk * a.v.head;
+  const uint16_t* kb = a.k.p + (long long)k0 * a.k.token + t.hk * a.k.head;
+  const uint16_t* vb = a.v.p + (long long)k0 * a.v.token + t.hk * a.v.head;
   bf16x8_t q[D / 16], g[D / 16];
   float delta = 0.f;
   {
     const long long row = q0 + r;
-    const uint16_t* qr = a.q.p + row * a.q.token + pl.hq * a.q.head + 8 * h;
-    const uint16_t* gr = b.dout.p + row * b.dout.token + pl.hq * b.dout.head + 8 * h;
-    const uint16_t* orow = a.o.p + row * a.o.token + pl.hq * a.o.head + 8 * h;
+    const uint16_t* qr = a.q.p + row * a.q.token + t.hq * a.q.head + 8 * h;
+    const uint16_t* gr = b.dout.p + row * b.dout.token + t.hq * b.dout.head + 8 * h;
+    const uint16_t* orow = a.o.p + row * a.o.token + t.hq * a.o.head + 8 * h;
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) {
       q[st] = as_bf16x8(ld16(qr + 16 * st));
@@ -457,10 +636,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
     }
     delta += __shfl_xor(delta, 32, kWave);
   }
-  const size_t stat = (size_t)pl.hq * a.Tq + q0 + r;
+  const size_t stat = (size_t)t.hq * a.Tq + q0 + r;
   const float lse = a.lse[stat];
-  const float lse2 = lse > -INFINITY ? lse * kLog2e : 0.f;  // a row that sees nothing: its scores are all -inf
-  if (pl.chunk == 0 && h == 0 && r0 + n <= last) {
+  const float lse2 = lse == -INFINITY ? 0.f : lse * kLog2e;  // a row that sees nothing: its scores are all -inf
+  if (t.chunk == 0 && h == 0 && r0 + n <= last) {
     b.lse2[stat] = lse2;
     b.delta[stat] = delta;
   }
@@ -523,13 +702,16 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardAr
     step(it, ldsK0, ldsV0, ldsK1, ldsV1);
     if (it + 1 < it1) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
-  if (ch.n > 1) {
-    float* part = b.q_part + ((size_t)(pl.chunk * slots + pl.slot) * a.Hq + pl.hq) * kAttnQ * D;
+  const bool mine = r0 + n <= last;
+  const uint32_t again = odd_rows<D>(dq, mine && lse == lse);
+  const bool whole = mine && !(again >> n & 1);
+  if (whole && t.chunks > 1) {
+    float* part = b.q_part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * kAttnQ * D;
     store_part<D>(part + (size_t)(32 * wave + n) * D, dq, h);
-    return;
+  } else if (whole) {
+    store_rows<D>(b.dq.p + (long long)(q0 + r) * b.dq.token + t.hq * b.dq.head, dq, a.scale, h);
   }
-  if (r0 + n <= last)
-    store_rows<D>(b.dq.p + (long long)(q0 + r) * b.dq.token + pl.hq * b.dq.head, dq, a.scale, h);
+  if (again) dq_again<D>(args_again<AttnBackwardArgs>(), slots, again, wave, lane, lse2, delta);
 }
 
 // Adds the chunks of the query tiles that were split, in order (see attn_fwd_join_k).
@@ -617,6 +799,69 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
   return t;
 }
 
+// Workgroup -> (key-value head, tile, chunk).  The sinks' tiles come first.  The chunk is the slowest index:
+// workgroups without work then lie together at the end (spread between the others they would leave
+// whole CUs idle).
+struct KvPlace {
+  int hk, chunk;
+  KvTile t;
+};
+template <int kBQ>
+__device__ __forceinline__ KvPlace kv_place(const AttnBackwardArgs& b, int slots, unsigned at) {
+  const int sinks = b.sink_tiles * b.f.n_seq, first = sinks * b.sink_splits;
+  int id = (int)(at / b.f.Hkv);
+  const bool sink = id < first;
+  if (!sink) id -= first;
+  const int n_tiles = sink ? sinks : slots, chunk = id / n_tiles;
+  return {(int)(at % b.f.Hkv), chunk, find_kv_tile<kBQ>(b, sink, slots, id - chunk * n_tiles)};
+}
+
+}  // namespace
+
+namespace {
+
+// attn_dkv_k's rows that are taken again: the wave's keys of the bits of `again`.
+template <int D>
+__device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, uint32_t again, int wave, int lane) {
+  constexpr int kBQ = attn_step(D);
+  const AttnArgs& a = b.f;
+  const KvPlace pl = kv_place<kBQ>(b, slots, group_again());
+  const KvTile& t = pl.t;
+  const int group = a.Hq / a.Hkv, it0 = pl.chunk * t.per, it1 = min(it0 + t.per, t.total);
+  const Mask m{t.k.n - t.q.n, a.window, a.sinks};
+  const float c = a.scale * kLog2e;
+  for (uint32_t left = again; left; left &= left - 1) {
+    const int at = 32 * wave + __builtin_ctz(left);
+    const long long key = t.k.lo + t.k0 + at;
+    const uint16_t* kp = a.k.p + key * a.k.token + pl.hk * a.k.head;
+    const uint16_t* vp = a.v.p + key * a.v.token + pl.hk * a.v.head;
+    RowSum<D> xk, xv;
+    for (int it = it0; it < it1 && !(xk.lost() && xv.lost()); ++it) {
+      const int hq = pl.hk * group + it / t.nt, i0 = (t.t_lo + t.nt - 1 - it % t.nt) * kBQ, row = i0 + lane;
+      const uint16_t* q = a.q.p + (long long)(t.q.lo + i0) * a.q.token + hq * a.q.head;
+      const uint16_t* g = b.dout.p + (long long)(t.q.lo + i0) * b.dout.token + hq * b.dout.head;
+      const bool see = lane < kBQ && row < t.q.n && sees(m, row + m.shift, t.k0 + at);
+      float w = 0.f, ds = 0.f;
+      if (see) {
+        const size_t stat = (size_t)hq * a.Tq + t.q.lo + row;
+        w = exp2_hw(fmaf(dot_rows<D>(q + lane * a.q.token, kp), c, -b.lse2[stat]));
+        ds = w * (dot_rows<D>(g + lane * b.dout.token, vp) - b.delta[stat]);
+      }
+      const uint64_t who = __ballot(see);
+      xv.add(who, w, g, b.dout.token, lane);
+      xk.add(who, ds, q, a.q.token, lane);
+    }
+    if (t.chunks > 1) {
+      float* part = b.part + ((size_t)(t.part + pl.chunk) * a.Hkv + pl.hk) * attn_part_floats(D) + (size_t)at * D;
+      xk.store_part(part, lane);
+      xv.store_part(part + (size_t)kAttnK * D, lane);
+    } else {
+      xk.store(b.dk.p + key * b.dk.token + pl.hk * b.dk.head, a.scale, lane);
+      xv.store(b.dv.p + key * b.dv.token + pl.hk * b.dv.head, 1.f, lane);
+    }
+  }
+}
+
 }  // namespace
 
 // dK and dV: a workgroup holds 128 keys of one key-value head, 32 per wave, and walks the queries
@@ -636,14 +881,9 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n = lane & 31;
   const int group = a.Hq / a.Hkv;
-  // The sinks' tiles come first.  The chunk is the slowest index: workgroups without work then lie
-  // together at the end (spread between the others they would leave whole CUs idle).
-  const int hk = (int)(blockIdx.x % a.Hkv), sinks = b.sink_tiles * a.n_seq, first = sinks * b.sink_splits;
-  int id = (int)(blockIdx.x / a.Hkv);
-  const bool sink = id < first;
-  if (!sink) id -= first;
-  const int n_tiles = sink ? sinks : slots, chunk = id / n_tiles;
-  const KvTile t = find_kv_tile<attn_step(D)>(b, sink, slots, id - chunk * n_tiles);
+  const KvPlace pl = kv_place<kBQ>(b, slots, blockIdx.x);
+  const KvTile& t = pl.t;
+  const int hk = pl.hk, chunk = pl.chunk;
   if (!t.ok || chunk >= t.chunks) return;
   const SeqRange qr = t.q, kr = t.k;
   const int k0 = t.k0, Lq = qr.n, Lk = kr.n, nt = t.nt;
@@ -751,28 +991,19 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
     step(it, ldsQ0, ldsG0, st0, ldsQ1, ldsG1, st1);
     if (it + 1 < it1) step(it + 1, ldsQ1, ldsG1, st1, ldsQ0, ldsG0, st0);
   }
-  if (t.chunks > 1) {
-    // fp32 sums [2][128][D] of this chunk
-    float* part = b.part + ((size_t)(t.part + chunk) * a.Hkv + hk) * attn_part_floats(D);
-#pragma unroll
-    for (int mb = 0; mb < D / 32; ++mb)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float* at = part + (size_t)(32 * wave + n) * D + 32 * mb + 8 * g + 4 * h;
-        f32x4_t x, y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = dk[mb][4 * g + i];
-          y[i] = dv[mb][4 * g + i];
-        }
-        *reinterpret_cast<f32x4_t*>(at) = x;
-        *reinterpret_cast<f32x4_t*>(at + (size_t)kAttnK * D) = y;
-      }
-    return;
+  const bool mine = j < Lk;
+  const uint32_t again = odd_rows<D>(dk, mine) | odd_rows<D>(dv, mine);
+  if (mine && !(again >> n & 1)) {
+    if (t.chunks > 1) {
+      float* part = b.part + ((size_t)(t.part + chunk) * a.Hkv + hk) * attn_part_floats(D) + (size_t)(32 * wave + n) * D;
+      store_part<D>(part, dk, h);
+      store_part<D>(part + (size_t)kAttnK * D, dv, h);
+    } else {
+      store_rows<D>(b.dk.p + (long long)(kr.lo + j) * b.dk.token + hk * b.dk.head, dk, a.scale, h);
+      store_rows<D>(b.dv.p + (long long)(kr.lo + j) * b.dv.token + hk * b.dv.head, dv, 1.f, h);
+    }
   }
-  if (j >= Lk) return;
-  store_rows<D>(b.dk.p + (long long)(kr.lo + j) * b.dk.token + hk * b.dk.head, dk, a.scale, h);
-  store_rows<D>(b.dv.p + (long long)(kr.lo + j) * b.dv.token + hk * b.dv.head, dv, 1.f, h);
+  if (again) dkv_again<D>(args_again<AttnBackwardArgs>(), slots, again, wave, lane);
 }
 
 // Adds the chunks of the key tiles that were split, in order: kJoinParts workgroups per tile.
