@@ -122,6 +122,35 @@ def test_absent_adapters_and_extreme_values(score):
     assert (idx != 2).all() and (idx != 3).all() and (idx == 4).any(1).all()
 
 
+@pytest.mark.parametrize("K,k", [(12, 2), (32, 4), (64, 5)])
+def test_chosen_scores_that_are_tiny(K, k):
+    """A bias that picks adapters far below the top, sigmoid scores near the smallest numbers: the
+    renormalised weights and their gradients stay those of the formula."""
+    m = need_gpu()
+    r = np.random.default_rng(K)
+    N = 70
+    low = np.arange(K) % 3 == 1
+    bias = np.where(low, 4.0, 0.0).astype(np.float32)
+    for score, at in (("softmax", -30.0), ("softmax", -86.0), ("softmax", -100.0), ("softmax", -120.0), ("sigmoid", -86.0),
+                      ("sigmoid", -100.0)):
+        l = r.normal(size=(N, K)).astype(np.float32)
+        l[:, low] += at
+        if low.sum() < k:
+            l[:, ~low] = -np.inf
+        kw = dict(bias=bias, score=score, renorm=True, factor=2.5)
+        # the choice among values that differ by far less than the bias's last bit goes by index on both sides
+        idx, w = run(m, l, k, **kw)
+        ri, rw = O.route_scores(l, k, **kw)
+        np.testing.assert_array_equal(idx, ri)
+        assert (np.abs(w - rw) <= rel_bound(l) * np.abs(rw) + 2.0 ** -126).all(), (score, at)
+        dw = r.normal(size=(N, k)).astype(np.float32)
+        got = host(m.molora_route_scores_backward(dev(l), dev(idx.astype(np.int32)), dev(dw),
+                                                  score=m.SCORE_SIGMOID if score == "sigmoid" else m.SCORE_SOFTMAX,
+                                                  renorm=True, factor=2.5))
+        ref, mag = O.route_scores_backward(l, idx, dw, score=score, renorm=True, factor=2.5)
+        assert (np.abs(got - ref) <= 3 * rel_bound(l) * mag + 2.0 ** -120).all(), (score, at)
+
+
 def test_output_of_another_operator_feeds_dispatch():
     m = need_gpu()
     l = np.random.default_rng(8).normal(size=(500, 12)).astype(np.float32)

@@ -3,8 +3,8 @@
 //
 //   s = softmax(l) | sigmoid(l);  c = s + bias;  mark_g = sum of group g's two largest c;
 //   keep the topk_group largest marks; choose the k largest c; w = factor s / [renorm] sum s
-//   dl_e = s_e (g_e - sum_j s_j g_j) | s_e (1 - s_e) g_e,
-//   g_j = factor (dw_j - [renorm] sum_i dw_i s_i / S) / [renorm] S over the chosen, S their sum
+//   dl_e = p_e (g_e - sum_j p_j g_j) [sigmoid: times 1 - s_e], g_j = factor dw_j of the chosen, else 0;
+//   renorm: p the chosen's s over their sum, 0 for the others; else p = s, for sigmoid without the sum
 //
 // Layout: eight lanes per token, lane i holding adapters [i E, (i + 1) E), E = 2, 4 or 8 with
 // 8 E >= K, so a wave takes eight tokens, a reduction over adapters is E register steps and
@@ -120,6 +120,36 @@ __device__ __forceinline__ void scores(const float* l, int score, F* s) {
   const F inv = total > F(0) ? F(1) / total : F(0);
 #pragma unroll
   for (int j = 0; j < E; ++j) s[j] *= inv;
+}
+
+// The scores s of the adapters in `sel` (bits of the lane's E) over their sum, 0 for the others.  With a
+// bias, or sigmoid scores, the chosen ones can all be tiny: a sum below 2^-60 is made again in 64 bits,
+// before fp32 loses bits to its smallest numbers and 1 / sum its range.
+template <int E>
+__device__ __forceinline__ void shares(const float* l, int score, uint32_t sel, bool mine, const float* s, float* p) {
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    p[j] = (sel >> j) & 1u ? s[j] : 0.f;
+    sum += p[j];
+  }
+  sum = sum8(sum);
+  const bool tiny = sum < 0x1p-60f;
+  const float inv = tiny ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int j = 0; j < E; ++j) p[j] *= inv;
+  if (!__any(mine && tiny)) return;
+  double d[E], total = 0;
+  scores<double, E>(l, score, d);
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    d[j] = (sel >> j) & 1u ? d[j] : 0.0;
+    total += d[j];
+  }
+  total = sum8(total);
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if (tiny) p[j] = total > 0.0 ? (float)(d[j] / total) : 0.f;
 }
 
 // Rounds of "largest value, lowest index" over the n values spread over eight lanes (lane i's
@@ -245,12 +275,7 @@ __global__ __launch_bounds__(kWave * kWaves) void route_scores_k(RouteScoresArgs
       chosen = choose<double, E>(s64, a, t, lane8, mem, &gap);
     }
   }
-  float sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < E; ++j)
-    if ((chosen >> (e0 + j)) & 1ull) sum += s[j];
-  sum = sum8(sum);
-  const float f = a.renorm ? (sum > 0.f ? a.factor / sum : 0.f) : a.factor;
+  if (a.renorm) shares<E>(l, a.score, (uint32_t)(chosen >> e0), mine && chosen != 0, s, s);
   if (!mine) return;
   int32_t* idx = a.idx + (size_t)tok * a.k;
   float* w = a.w + (size_t)tok * a.k;
@@ -259,7 +284,7 @@ __global__ __launch_bounds__(kWave * kWaves) void route_scores_k(RouteScoresArgs
     if ((chosen >> (e0 + j)) & 1ull) {
       const int slot = __popcll(chosen & ((1ull << (e0 + j)) - 1));  // ascending adapter index
       idx[slot] = e0 + j;
-      w[slot] = s[j] * f;
+      w[slot] = s[j] * a.factor;
     }
   if (lane8 >= __popcll(chosen) && lane8 < a.k) {
     idx[lane8] = -1;
@@ -291,26 +316,21 @@ __global__ __launch_bounds__(kWave * kWaves) void route_scores_bwd_k(RouteScores
           sel |= 1u << j;
         }
     }
-  float sum = 0.f, dot = 0.f;  // of the chosen: s, s g
+  // softmax: p (g - sum p g); sigmoid the same times 1 - s, the sum only with renorm.  p: s, or its share
+  float p[E], dot = 0.f;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    if ((sel >> j) & 1u) sum += s[j];
-    dot = fmaf(s[j], g[j], dot);
-  }
-  sum = sum8(sum);
-  dot = sum8(dot);
-  if (a.renorm) {
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  for (int j = 0; j < E; ++j) p[j] = s[j];
+  if (a.renorm) shares<E>(l, a.score, sel, mine, s, p);
 #pragma unroll
-    for (int j = 0; j < E; ++j) g[j] = ((sel >> j) & 1u) ? (g[j] - dot * inv) * inv : 0.f;
-    dot = 0.f;  // sum of s g over the chosen: zero by construction
-  }
+  for (int j = 0; j < E; ++j) dot = fmaf(p[j], g[j], dot);
+  dot = a.renorm || a.score == kScoreSoftmax ? sum8(dot) : 0.f;
   if (!mine) return;
   float* out = dl + (size_t)tok * a.K + e0;
   float r[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
-    r[j] = a.score == kScoreSigmoid ? s[j] * (1.f - s[j]) * g[j] : s[j] * (g[j] - dot);
+    r[j] = p[j] * (g[j] - dot);
+    if (a.score == kScoreSigmoid) r[j] *= 1.f - s[j];
     if (!(l[j] > -INFINITY)) r[j] = 0.f;
   }
   if (a.K == kLanes * E) {
