@@ -185,9 +185,11 @@ __device__ __forceinline__ bool sees_all(const Mask& m, int p_lo, int p_hi, int 
 
 // ---- Rows taken again.  A hidden pair has weight 0, but 0 times an infinity or a NaN is NaN, so a row of
 // sums that is not finite may owe it to a row that it does not see and that shares a tile with one
-// that it does.  Such rows are summed again over the visible pairs alone, a lane per pair for the
-// weights and then a lane per column.  Finite inputs never come here; the test itself is within the
-// spread of the measurements (train batch 270 us without it, 268 us with it).
+// that it does.  Its columns that are not finite are summed again over the visible pairs alone, a lane
+// per pair for the weights and then a lane per column.  Columns with such a value in a tile that the
+// whole wave sees are lost for good: one pass over those tiles leaves them out, so that only the rows
+// around a bad one are taken again.  Finite inputs never come here; the test itself is within the spread
+// of the measurements (train batch 270 us without it, 268 us with it).
 
 // The workgroup's number and the kernel's first argument, read afresh where rows are taken again:
 // otherwise all they lead to would be kept in scalar registers, and spilled, while the products run (8192
@@ -227,7 +229,7 @@ __device__ __forceinline__ bool sees(const Mask& m, int p, int j) {
 template <int D>
 __device__ __forceinline__ float dot_rows(const uint16_t* x, const uint16_t* y) {
   float s = 0.f;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = 0; i < D; i += 8) {
     const u32x4_t u = ld16(x + i), v = ld16(y + i);
 #pragma unroll
@@ -243,6 +245,33 @@ __device__ __forceinline__ float lane_value(float v, int i) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
 }
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// The lane's D / 64 columns (bits) in which one of the first n rows of `base` is not finite.
+template <int D>
+__device__ __forceinline__ uint32_t odd_columns(const uint16_t* base, long long stride, int n, int lane) {
+  uint32_t odd = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      odd |= (uint32_t)((base[i * stride + D / 64 * lane + c] & 0x7f80) == 0x7f80) << c;
+  return odd;
+}
+
+// The lane's columns of a stored row that are not finite and not lost.
+template <int D, typename T>
+__device__ __forceinline__ uint32_t to_repair(const T* row, uint32_t lost, int lane) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const T v = row[D / 64 * lane + c];
+    if constexpr (sizeof(T) == 2) odd |= (uint32_t)!finite(bf16_to_f32(v)) << c;
+    else odd |= (uint32_t)!finite(v) << c;
+  }
+  return odd & ~lost;
+}
+
 // One row of sums, D / 64 columns per lane.
 template <int D>
 struct RowSum {
@@ -256,20 +285,16 @@ struct RowSum {
       for (int c = 0; c < D / 64; ++c) x[c] = fmaf(f, bf16_to_f32(base[i * stride + D / 64 * lane + c]), x[c]);
     }
   }
-  // Nothing that is added can change it.
-  __device__ __forceinline__ bool lost() const {
-    bool nan = true;
+  // The columns of `odd`.
+  __device__ __forceinline__ void store(uint16_t* row, float mul, uint32_t odd, int lane) const {
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) nan &= x[c] != x[c];
-    return __all(nan);
+    for (int c = 0; c < D / 64; ++c)
+      if (odd >> c & 1) row[D / 64 * lane + c] = (uint16_t)pack_bf16x2(x[c] * mul, 0.f);
   }
-  __device__ __forceinline__ void store(uint16_t* row, float mul, int lane) const {
+  __device__ __forceinline__ void store(float* row, float, uint32_t odd, int lane) const {
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) row[D / 64 * lane + c] = (uint16_t)pack_bf16x2(x[c] * mul, 0.f);
-  }
-  __device__ __forceinline__ void store_part(float* row, int lane) const {
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) row[D / 64 * lane + c] = x[c];
+    for (int c = 0; c < D / 64; ++c)
+      if (odd >> c & 1) row[D / 64 * lane + c] = x[c];
   }
 };
 
@@ -301,6 +326,17 @@ struct QTile {
   int hq, hk, slot, chunk, chunks, it0, it1;
   int q0, k0, Lk, last, row0;  // first rows of the sequence, keys, last query, tile's first query
   bool ok;
+  // The lane's columns of `base` that are not finite in a key tile which all of the wave's rows see.
+  template <int D>
+  __device__ __forceinline__ uint32_t lost_columns(const uint16_t* base, long long stride, int wave, int lane) const {
+    const int r0 = row0 + 32 * wave, p_lo = r0 + m.shift, p_hi = min(r0 + 31, last) + m.shift;
+    uint32_t odd = 0;
+    for (int it = it0; it < it1; ++it) {
+      const int j0 = kt.at(it);
+      if (sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1)) odd |= odd_columns<D>(base + j0 * stride, stride, kBN, lane);
+    }
+    return odd;
+  }
 };
 __device__ __forceinline__ QTile q_tile(const AttnArgs& a, int slots, unsigned id, int splits) {
   QTile x{};
@@ -360,22 +396,28 @@ __device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t
   const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + t.hk * a.k.head;
   const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + t.hk * a.v.head;
   const float c = a.scale * kLog2e;
+  const uint32_t lost = t.lost_columns<D>(vb, a.v.token, wave, lane);
+  __threadfence();  // the rows are stored
   for (uint32_t left = again; left; left &= left - 1) {
     const int i = __builtin_ctz(left), at = 32 * wave + i, p = t.row0 + at + t.m.shift;
     const long long row = t.q0 + t.row0 + at;
     const uint16_t* qr = a.q.p + row * a.q.token + t.hq * a.q.head;
     const float top = lane_value(mx, i), ref = top > -INFINITY ? top : 0.f;
-    RowSum<D> x;
-    for (int it = t.it0; it < t.it1 && !x.lost(); ++it) {
-      const int j0 = t.kt.at(it), j = j0 + lane;
-      const bool see = sees(t.m, p, j);
-      const float w = see ? exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -ref)) : 0.f;
-      x.add(__ballot(see), w, vb + j0 * a.v.token, a.v.token, lane);
-    }
+    auto repair = [&](auto* out) {
+      const uint32_t odd = to_repair<D>(out, lost, lane);
+      if (!__any(odd)) return;
+      RowSum<D> x;
+      for (int it = t.it0; it < t.it1; ++it) {
+        const int j0 = t.kt.at(it), j = j0 + lane;
+        const bool see = sees(t.m, p, j);
+        const float w = see ? exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -ref)) : 0.f;
+        x.add(__ballot(see), w, vb + j0 * a.v.token, a.v.token, lane);
+      }
+      x.store(out, lane_value(inv, i), odd, lane);
+    };
     if (t.chunks > 1)
-      x.store_part(a.part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * attn_fwd_part_floats(D) + (size_t)at * D,
-                   lane);
-    else x.store(a.o.p + row * a.o.token + t.hq * a.o.head, lane_value(inv, i), lane);
+      repair(a.part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * attn_fwd_part_floats(D) + (size_t)at * D);
+    else repair(a.o.p + row * a.o.token + t.hq * a.o.head);
   }
 }
 
@@ -479,17 +521,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   sum += __shfl_xor(sum, 32, kWave);
   const bool mine = r0 + n <= last;
   const uint32_t again = odd_rows<D>(o, mine && sum < INFINITY);
-  const bool whole = mine && !(again >> n & 1);
   const float inv = sum > 0.f ? 1.f / sum : sum;
   if (t.chunks > 1) {  // sums [128][D], maxima [128], weights [128] of this chunk
     float* part = a.part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * attn_fwd_part_floats(D);
-    if (whole) store_part<D>(part + (size_t)(32 * wave + n) * D, o, h);
+    if (mine) store_part<D>(part + (size_t)(32 * wave + n) * D, o, h);
     if (h == 0) {
       part[(size_t)kAttnQ * D + 32 * wave + n] = mx;
       part[(size_t)kAttnQ * (D + 1) + 32 * wave + n] = sum;
     }
   } else {
-    if (whole) store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + t.hq * a.o.head, o, inv, h);
+    if (mine) store_rows<D>(a.o.p + (long long)(q0 + r) * a.o.token + t.hq * a.o.head, o, inv, h);
     if (mine && a.lse != nullptr && h == 0)
       a.lse[(size_t)t.hq * a.Tq + q0 + r] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
   }
@@ -572,26 +613,32 @@ __device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, u
   const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + t.hk * a.k.head;
   const uint16_t* vb = a.v.p + (long long)t.k0 * a.v.token + t.hk * a.v.head;
   const float c = a.scale * kLog2e;
+  const uint32_t lost = t.lost_columns<D>(kb, a.k.token, wave, lane);
+  __threadfence();  // the rows are stored
   for (uint32_t left = again; left; left &= left - 1) {
     const int i = __builtin_ctz(left), at = 32 * wave + i, p = t.row0 + at + t.m.shift;
     const long long row = t.q0 + t.row0 + at;
     const uint16_t* qr = a.q.p + row * a.q.token + t.hq * a.q.head;
     const uint16_t* gr = b.dout.p + row * b.dout.token + t.hq * b.dout.head;
     const float li = lane_value(lse2, i), di = lane_value(delta, i);
-    RowSum<D> x;
-    for (int it = t.it0; it < t.it1 && !x.lost(); ++it) {
-      const int j0 = t.kt.at(it), j = j0 + lane;
-      const bool see = sees(t.m, p, j);
-      float w = 0.f;
-      if (see) {
-        w = exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -li));
-        w *= dot_rows<D>(gr, vb + j * a.v.token) - di;
+    auto repair = [&](auto* out) {
+      const uint32_t odd = to_repair<D>(out, lost, lane);
+      if (!__any(odd)) return;
+      RowSum<D> x;
+      for (int it = t.it0; it < t.it1; ++it) {
+        const int j0 = t.kt.at(it), j = j0 + lane;
+        const bool see = sees(t.m, p, j);
+        float w = 0.f;
+        if (see) {
+          w = exp2_hw(fmaf(dot_rows<D>(qr, kb + j * a.k.token), c, -li));
+          w *= dot_rows<D>(gr, vb + j * a.v.token) - di;
+        }
+        x.add(__ballot(see), w, kb + j0 * a.k.token, a.k.token, lane);
       }
-      x.add(__ballot(see), w, kb + j0 * a.k.token, a.k.token, lane);
-    }
-    if (t.chunks > 1)
-      x.store_part(b.q_part + (((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * kAttnQ + at) * D, lane);
-    else x.store(b.dq.p + row * b.dq.token + t.hq * b.dq.head, a.scale, lane);
+      x.store(out, a.scale, odd, lane);
+    };
+    if (t.chunks > 1) repair(b.q_part + (((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * kAttnQ + at) * D);
+    else repair(b.dq.p + row * b.dq.token + t.hq * b.dq.head);
   }
 }
 
@@ -703,12 +750,12 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(Att
     if (it + 1 < it1) step(it + 1, ldsK1, ldsV1, ldsK0, ldsV0);
   }
   const bool mine = r0 + n <= last;
-  const uint32_t again = odd_rows<D>(dq, mine && lse == lse);
-  const bool whole = mine && !(again >> n & 1);
-  if (whole && t.chunks > 1) {
+  // a row that sees something and whose lse or delta is not finite has no other result
+  const uint32_t again = odd_rows<D>(dq, mine && (lse == -INFINITY || finite(lse + delta)));
+  if (mine && t.chunks > 1) {
     float* part = b.q_part + ((size_t)(t.chunk * slots + t.slot) * a.Hq + t.hq) * kAttnQ * D;
     store_part<D>(part + (size_t)(32 * wave + n) * D, dq, h);
-  } else if (whole) {
+  } else if (mine) {
     store_rows<D>(b.dq.p + (long long)(q0 + r) * b.dq.token + t.hq * b.dq.head, dq, a.scale, h);
   }
   if (again) dq_again<D>(args_again<AttnBackwardArgs>(), slots, again, wave, lane, lse2, delta);
@@ -827,37 +874,62 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
   const AttnArgs& a = b.f;
   const KvPlace pl = kv_place<kBQ>(b, slots, group_again());
   const KvTile& t = pl.t;
-  const int group = a.Hq / a.Hkv, it0 = pl.chunk * t.per, it1 = min(it0 + t.per, t.total);
+  const int group = a.Hq / a.Hkv, it0 = pl.chunk * t.per, it1 = min(it0 + t.per, t.total), jw = t.k0 + 32 * wave;
   const Mask m{t.k.n - t.q.n, a.window, a.sinks};
   const float c = a.scale * kLog2e;
+  struct Step {
+    const uint16_t *q, *g;
+    const float *lse2, *delta;
+    int i0;  // first row
+  };
+  auto at = [&](int it) {
+    const int hq = pl.hk * group + it / t.nt, i0 = (t.t_lo + t.nt - 1 - it % t.nt) * kBQ;
+    const long long row = t.q.lo + i0;
+    const size_t stat = (size_t)hq * a.Tq + row;
+    return Step{a.q.p + row * a.q.token + hq * a.q.head, b.dout.p + row * b.dout.token + hq * b.dout.head, b.lse2 + stat,
+                b.delta + stat, i0};
+  };
+  uint32_t lost_k = 0, lost_v = 0;
+  for (int it = it0; it < it1; ++it) {
+    const Step s = at(it);
+    const int p0 = s.i0 + m.shift;
+    if (s.i0 + kBQ > t.q.n || !sees_all(m, p0, p0 + kBQ - 1, jw, jw + 31)) continue;
+    const bool bad_p = __any(lane < kBQ && !finite(s.lse2[lane % kBQ]));
+    const bool bad_ds = bad_p || __any(lane < kBQ && !finite(s.delta[lane % kBQ]));
+    lost_v |= bad_p ? ~0u : odd_columns<D>(s.g, b.dout.token, kBQ, lane);
+    lost_k |= bad_ds ? ~0u : odd_columns<D>(s.q, a.q.token, kBQ, lane);
+  }
+  __threadfence();  // the rows are stored
   for (uint32_t left = again; left; left &= left - 1) {
-    const int at = 32 * wave + __builtin_ctz(left);
-    const long long key = t.k.lo + t.k0 + at;
+    const int j = jw + __builtin_ctz(left);
+    const long long key = t.k.lo + j;
     const uint16_t* kp = a.k.p + key * a.k.token + pl.hk * a.k.head;
     const uint16_t* vp = a.v.p + key * a.v.token + pl.hk * a.v.head;
-    RowSum<D> xk, xv;
-    for (int it = it0; it < it1 && !(xk.lost() && xv.lost()); ++it) {
-      const int hq = pl.hk * group + it / t.nt, i0 = (t.t_lo + t.nt - 1 - it % t.nt) * kBQ, row = i0 + lane;
-      const uint16_t* q = a.q.p + (long long)(t.q.lo + i0) * a.q.token + hq * a.q.head;
-      const uint16_t* g = b.dout.p + (long long)(t.q.lo + i0) * b.dout.token + hq * b.dout.head;
-      const bool see = lane < kBQ && row < t.q.n && sees(m, row + m.shift, t.k0 + at);
-      float w = 0.f, ds = 0.f;
-      if (see) {
-        const size_t stat = (size_t)hq * a.Tq + t.q.lo + row;
-        w = exp2_hw(fmaf(dot_rows<D>(q + lane * a.q.token, kp), c, -b.lse2[stat]));
-        ds = w * (dot_rows<D>(g + lane * b.dout.token, vp) - b.delta[stat]);
+    auto repair = [&](auto* dk, auto* dv) {
+      const uint32_t odd_k = to_repair<D>(dk, lost_k, lane), odd_v = to_repair<D>(dv, lost_v, lane);
+      if (!__any(odd_k | odd_v)) return;
+      RowSum<D> xk, xv;
+      for (int it = it0; it < it1; ++it) {
+        const Step s = at(it);
+        const int row = s.i0 + lane;
+        const bool see = lane < kBQ && row < t.q.n && sees(m, row + m.shift, j);
+        float w = 0.f, ds = 0.f;
+        if (see) {
+          w = exp2_hw(fmaf(dot_rows<D>(s.q + lane * a.q.token, kp), c, -s.lse2[lane]));
+          ds = w * (dot_rows<D>(s.g + lane * b.dout.token, vp) - s.delta[lane]);
+        }
+        const uint64_t who = __ballot(see);
+        xv.add(who, w, s.g, b.dout.token, lane);
+        xk.add(who, ds, s.q, a.q.token, lane);
       }
-      const uint64_t who = __ballot(see);
-      xv.add(who, w, g, b.dout.token, lane);
-      xk.add(who, ds, q, a.q.token, lane);
-    }
+      xk.store(dk, a.scale, odd_k, lane);
+      xv.store(dv, 1.f, odd_v, lane);
+    };
     if (t.chunks > 1) {
-      float* part = b.part + ((size_t)(t.part + pl.chunk) * a.Hkv + pl.hk) * attn_part_floats(D) + (size_t)at * D;
-      xk.store_part(part, lane);
-      xv.store_part(part + (size_t)kAttnK * D, lane);
+      float* part = b.part + ((size_t)(t.part + pl.chunk) * a.Hkv + pl.hk) * attn_part_floats(D) + (size_t)(j - t.k0) * D;
+      repair(part, part + (size_t)kAttnK * D);
     } else {
-      xk.store(b.dk.p + key * b.dk.token + pl.hk * b.dk.head, a.scale, lane);
-      xv.store(b.dv.p + key * b.dv.token + pl.hk * b.dv.head, 1.f, lane);
+      repair(b.dk.p + key * b.dk.token + pl.hk * b.dk.head, b.dv.p + key * b.dv.token + pl.hk * b.dv.head);
     }
   }
 }
@@ -993,7 +1065,7 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   }
   const bool mine = j < Lk;
   const uint32_t again = odd_rows<D>(dk, mine) | odd_rows<D>(dv, mine);
-  if (mine && !(again >> n & 1)) {
+  if (mine) {
     if (t.chunks > 1) {
       float* part = b.part + ((size_t)(t.part + chunk) * a.Hkv + hk) * attn_part_floats(D) + (size_t)(32 * wave + n) * D;
       store_part<D>(part, dk, h);
