@@ -186,6 +186,20 @@ def test_backward(score, renorm, N, K, k):
     assert (got[~(l > -np.inf)] == 0).all()
 
 
+@pytest.mark.parametrize("score", SCORES)
+def test_a_single_renormalised_weight_is_constant(score):
+    """k = 1 with renorm: the weight is the factor itself, whatever the logits, and the gradient exactly 0."""
+    m = need_gpu()
+    r = np.random.default_rng(13)
+    l = (3 * r.normal(size=(400, 36))).astype(np.float32)
+    idx, w = run(m, l, 1, score=score, factor=2.5)
+    assert (w == 2.5).all()
+    dw = r.normal(size=(400, 1)).astype(np.float32)
+    got = m.molora_route_scores_backward(dev(l), dev(idx.astype(np.int32)), dev(dw), factor=2.5,
+                                         score=m.SCORE_SIGMOID if score == "sigmoid" else m.SCORE_SOFTMAX)
+    assert (got == 0).all()
+
+
 def test_backward_against_differences():
     m = need_gpu()
     r = np.random.default_rng(11)

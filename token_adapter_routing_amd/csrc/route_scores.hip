@@ -124,7 +124,8 @@ __device__ __forceinline__ void scores(const float* l, int score, F* s) {
 
 // The scores s of the adapters in `sel` (bits of the lane's E) over their sum, 0 for the others.  With a
 // bias, or sigmoid scores, the chosen ones can all be tiny: a sum below 2^-60 is made again in 64 bits,
-// before fp32 loses bits to its smallest numbers and 1 / sum its range.
+// before fp32 loses bits to its smallest numbers and 1 / sum its range.  A single chosen adapter's share is
+// exactly 1 (the quotient is corrected once), so that its weight has no gradient.
 template <int E>
 __device__ __forceinline__ void shares(const float* l, int score, uint32_t sel, bool mine, const float* s, float* p) {
   float sum = 0.f;
@@ -137,7 +138,10 @@ __device__ __forceinline__ void shares(const float* l, int score, uint32_t sel, 
   const bool tiny = sum < 0x1p-60f;
   const float inv = tiny ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int j = 0; j < E; ++j) p[j] *= inv;
+  for (int j = 0; j < E; ++j) {
+    const float q = p[j] * inv;
+    p[j] = tiny ? 0.f : fmaf(fmaf(-q, sum, p[j]), inv, q);
+  }
   if (!__any(mine && tiny)) return;
   double d[E], total = 0;
   scores<double, E>(l, score, d);
