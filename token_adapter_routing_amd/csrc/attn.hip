@@ -423,7 +423,17 @@ __device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t
 
 }  // namespace
 
-// A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.
+// A workgroup: 128 queries of one head, 32 per wave; tiles of 64 keys, double-buffered.  128 queries
+// because a tile of keys then feeds four waves from LDS once, and the operands, sums and scores of 32
+// queries by 128 values are the 223 registers that leave two waves per SIMD; 64 keys because two
+// workgroups' double buffers of K and V (64 KiB each) then fit a CU.
+//
+// Bound by the issue of matrix and vector instructions together (per 64 keys a wave has 32 products of
+// 32 cycles at two waves per SIMD, and about 190 vector instructions of softmax between them) and by
+// the clock they leave (about 1.8 GHz): 8192 tokens, 32 / 8 heads of 128, 533 us = 1031 TFLOP/s, the
+// matrix units busy 54 % of the cycles, no bank conflicts; without copies and barriers the rest takes
+// 479 us.  Heads of 64 do half the products per softmax: 4 x 4096 tokens, 16 heads 179 us = 768 TFLOP/s.
+// Short calls: one tile 8.6 us, each further 64 keys about 1.07 us.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
@@ -645,7 +655,11 @@ __device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, u
 }  // namespace
 
 // dQ and the row sums of dO O: a workgroup holds 128 queries of one head, 32 per wave, and walks
-// the keys as the forward does.
+// the keys as the forward does.  A kernel of its own, so that dQ is summed in registers in one order:
+// together with dK and dV it would need atomics or a pass over partial sums.  The price is S and dP
+// twice, seven products for five.
+// Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 740 us = 1113 TFLOP/s, the matrix units busy
+// 60 % of the cycles (three products for one exponential); heads of 64, window 1024: 128 us.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
@@ -940,14 +954,18 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
 // of every query head that reads it (or one chunk of them, whose sums go to the workspace).  S and
 // dP are computed with the queries down, so that P and dS are the right operands of dV^T = dO^T P
 // and dK^T = Q^T dS.
+// Bound as the forward, and by the waits between steps: 8192 tokens, 32 / 8 heads of 128, 1150 us = 956
+// TFLOP/s, the matrix units busy 48 % of the cycles, waves waiting for copies and each other 28 %
+// (with 128 values a step holds 32 rows: Q, dO and V fill the LDS of two workgroups); heads of 64,
+// 64 rows per step, 4 x 4096 tokens, 16 heads 318 us = 866 TFLOP/s.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kBQ = attn_step(D), kTileB = kBQ * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
   __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
   // The workgroup's V stays in LDS: beside K's operands and the sums of dK and dV in registers it would
-  // cost a wave per SIMD (4 x 4096 tokens, 16 heads of 64: 451 us with V in registers and two waves,
-  // 402 us with three; heads of 128: two waves instead of one, 1438 -> 794 us).
+  // cost a wave per SIMD (4 x 4096 tokens, 16 heads, when it was moved: 64 values 451 us with V in
+  // registers and two waves, 402 us with three; 128 values 1438 us with one wave, 794 us with two).
   __shared__ __attribute__((aligned(16))) char ldsV[kAttnK * Tile<D>::kRow];
   const AttnArgs& a = b.f;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
@@ -1078,7 +1096,8 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   if (again) dkv_again<D>(args_again<AttnBackwardArgs>(), slots, again, wave, lane);
 }
 
-// Adds the chunks of the key tiles that were split, in order: kJoinParts workgroups per tile.
+// Adds the chunks of the key tiles that were split, in order: kJoinParts workgroups per tile.  Bound by
+// the parts' bytes: 8192 tokens, 8 heads of 128 in 2 chunks, 134 MB in 19 us.
 constexpr int kJoinParts = 16;
 template <int D>
 __global__ __launch_bounds__(256) void attn_dkv_join_k(AttnBackwardArgs b, int slots) {

@@ -6,7 +6,9 @@
 namespace molora {
 
 // Splits: enough workgroups (kDecTarget) that sequences of different lengths even out over the
-// 256 CUs, no more than the longest possible sequence has pieces of kDecMinBlocks blocks.
+// 256 CUs, no more than the longest possible sequence has pieces of kDecMinBlocks blocks.  64 ragged
+// sequences of up to 8192, 8 key-value heads: 239 / 214 / 203 / 207 us with 512 / 1024 / 2048 / 4096; one
+// of 32771: 31.4 / 30.2 / 30.0 / 29.8 us.
 DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int page_size, int table_width) {
   constexpr long long kDecTarget = 2048;
   DecodePlan p{};
@@ -44,10 +46,10 @@ size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, 
 
 // A causal sequence's key tiles are seen by unequal numbers of queries, so with few tiles the longest
 // one sets the time: chunks until there are kBwdTarget workgroups, two for each of the 512 places
-// that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 2127 us unsplit, 1525 us
-// in 4 chunks).  With a window a tile sees a window's worth, but the sinks' tiles every query: those
-// are taken apart, in up to 16 chunks (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: 2300 us
-// unsplit, 373 us in 15 chunks).
+// that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 1575 us unsplit, 1162 us
+// and 19 us for the join in 2 chunks).  With a window a tile sees a window's worth, but the sinks' tiles every query: those
+// are taken apart, in up to 16 chunks (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: 1008 us
+// unsplit, 198 us and 5 us for the join in 16 chunks).
 AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks) {
   constexpr long long kBwdTarget = 1024, kBwdPartBytes = 512ll << 20;
   AttnBwdPlan p{};

@@ -9,7 +9,13 @@
 // Layout: eight lanes per token, lane i holding adapters [i E, (i + 1) E), E = 2, 4 or 8 with
 // 8 E >= K, so a wave takes eight tokens, a reduction over adapters is E register steps and
 // three exchanges inside eight lanes, and each lane's logits are one contiguous piece.  One
-// round of the selection per chosen adapter (k <= 8).
+// round of the selection per chosen adapter (k <= 8).  Eight lanes and not a wave per token: a
+// reduction over 64 lanes is six dependent exchanges for one token, this is three for eight.
+//
+// Bound by the length of that chain, not by memory (16384 x 64 fp32 logits are 4.3 MB, 1 us):
+//   scores  256 x 16, k 2: 3.0 us; 16384 x 64, k 8, 8 groups of which 4, bias: 8.8 us (10.1 us with
+//           LDS exchanges for the register moves)
+//   backward  16384 x 64, k 4: 4.9 us, 1.8 TB/s
 #include <cfloat>
 #include <cmath>
 
