@@ -38,6 +38,18 @@ __device__ __forceinline__ int wave_search(int n, long long x, Key key) {
   }
 }
 
+// Sum over lanes 0..15, uniform.
+template <int CTRL>
+__device__ __forceinline__ int row_ror(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, true);
+}
+__device__ __forceinline__ int row_sum16(int v) {
+  v += row_ror<0x128>(v);
+  v += row_ror<0x124>(v);
+  v += row_ror<0x122>(v);
+  return __builtin_amdgcn_readfirstlane(v + row_ror<0x121>(v));
+}
+
 // Row range of one sequence, limited to [0, T].
 struct SeqRange {
   int lo, n;
@@ -55,12 +67,15 @@ struct SeqTile {
   bool ok;
 };
 
-// kRanked sequences at most: the longest sequence's tiles come first (workgroups start in slot order, so
-// long ones do not come last), FROM_END: its last tile first.  The search is a step per sequence,
-// which with more would cost what the order gains (32 sequences of 512 tokens: 83 us in slot order,
-// 98 us ranked).
-// With more, slots run through the sequences (attn_slot0).  Up to 64 the lanes hold one each.
-constexpr int kRanked = 16;
+// Up to kLevels sequences: the longest tiles of all sequences come first, by how many tiles lie between a
+// tile and its sequence's shortest end (workgroups start in slot order, so long ones do not come last and
+// the first ones are spread over the CUs).  FROM_END: a sequence's last tile is its longest.  The level of
+// a slot is found by halving, a sum over 16 lanes per step (4 x 2048 tokens, 16 heads of 64: 64 us
+// forward and 182 us backward sequence by sequence, 55 and 156 us by level).
+// With more, slots run through the sequences (attn_slot0), which are then short beside the batch, and the
+// tiles of one, which read the same rows, run together (32 x 512 tokens, 16 heads of 128: 77 and 257 us, by
+// level 85 and 279 us).  Up to 64 the lanes hold one each.
+constexpr int kLevels = 16;
 template <bool OF_A, bool FROM_END, int TILE>
 __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ offa, int Ta, const int32_t* __restrict__ offb,
                                              int Tb, int n_seq, int slots, int slot) {
@@ -90,17 +105,25 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ offa, i
   const SeqRange mine = OF_A ? a : b;
   const int n = (mine.n + TILE - 1) / TILE;
   int s, tile;
-  if (n_seq <= kRanked) {
-    int first = 0;  // tiles of the sequences before this one
-    for (int i = 0; i < n_seq; ++i) {
-      const int m = __builtin_amdgcn_readlane(n, i);
-      first += (m > n || (m == n && i < lane)) ? m : 0;
+  if (n_seq <= kLevels) {
+    // level l of a tile: how many of its sequence, itself included, are as long or shorter; above(l): how
+    // many tiles of all have a higher one
+    auto above = [&](int l) { return row_sum16(max(n - l, 0)); };
+    if (slot >= above(0)) return t;
+    int lo = 0, hi = 1;  // in the end above(lo) > slot >= above(hi), hi = lo + 1
+    while (above(hi) > slot) {
+      lo = hi;
+      hi *= 2;
     }
-    const uint64_t here = __ballot(first <= slot && slot < first + n);
-    if (here == 0) return t;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (above(mid) > slot) lo = mid;
+      else hi = mid;
+    }
+    uint64_t here = __ballot(n >= hi);
+    for (int skip = slot - above(hi); skip > 0; --skip) here &= here - 1;
     s = __builtin_ctzll(here);
-    tile = slot - __builtin_amdgcn_readlane(first, s);
-    if (FROM_END) tile = __builtin_amdgcn_readlane(n, s) - 1 - tile;
+    tile = FROM_END ? hi - 1 : __builtin_amdgcn_readlane(n, s) - hi;
   } else {
     if (FROM_END) slot = slots - 1 - slot;
     const int first = (int)attn_slot0(mine.lo, lane, TILE);
