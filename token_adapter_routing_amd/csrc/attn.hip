@@ -852,7 +852,7 @@ __device__ __forceinline__ KvTile find_kv_tile(const AttnBackwardArgs& b, bool s
   t.nt = max((i_hi + kBQ - 1) / kBQ - t.t_lo, 0);
   t.total = t.nt * group;
   const int steps = (t.q.n + kBQ - 1) / kBQ * group, splits = sink ? b.sink_splits : b.splits;
-  t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, 1024 / kBQ);
+  t.per = max(((sink ? steps : min(steps, b.most)) + splits - 1) / splits, sink ? b.sink_min : b.min_steps);
   t.per = max(t.per, (t.total + splits - 1) / splits);  // never more chunks than there are places
   t.chunks = max((t.total + t.per - 1) / t.per, 1);
   const long long sink_parts = (long long)b.sink_tiles * a.n_seq * b.sink_splits;

@@ -271,6 +271,8 @@ int molora_attn_backward(const molora_attn_shape* shape, const molora_rows* dout
   b.sink_splits = plan.sink_splits;
   b.sink_tiles = plan.sink_tiles;
   b.most = plan.most;
+  b.min_steps = plan.min_steps;
+  b.sink_min = plan.sink_min;
   const hipError_t e = molora::launch_attn_backward(b, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attn_backward launch");
 }

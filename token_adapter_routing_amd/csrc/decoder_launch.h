@@ -47,7 +47,7 @@ struct AttnBackwardArgs {
   float* delta;  // workspace [Hq][Tq]: rowsum(dO O)
   int q_splits;   // attn_q_splits
   float* q_part;  // workspace: the split query tiles' sums
-  int splits, sink_splits, sink_tiles, most;  // attn_bwd_plan
+  int splits, sink_splits, sink_tiles, most, min_steps, sink_min;  // attn_bwd_plan
   float* part;   // workspace: the split key tiles' sums
 };
 hipError_t launch_attn_backward(const AttnBackwardArgs& a, hipStream_t s);

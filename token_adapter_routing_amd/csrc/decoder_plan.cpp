@@ -28,8 +28,8 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
 // themselves fill the GPU.  A tile cannot be told to be long from here: sequences of kQKeys keys on
 // average are (512 keys gain nothing: 15.8 us whole, 17.1 us split; 1024 keys 24.4 us whole, 18.4 us
 // split).
+constexpr long long kQTarget = 512, kQKeys = 768;
 int attn_q_splits(int Tq, int Tkv, int n_seq, int n_heads, int window, int sinks) {
-  constexpr long long kQTarget = 512, kQKeys = 768;
   const long long units = attn_slots(Tq, n_seq, kAttnQ) * n_heads;
   if (units <= 0 || units >= kQTarget / 2 || Tkv < kQKeys * n_seq) return 1;
   long long keys = Tkv;
@@ -47,30 +47,36 @@ size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, 
 // A causal sequence's key tiles are seen by unequal numbers of queries, so with few tiles the longest
 // one sets the time: chunks until there are kBwdTarget workgroups, two for each of the 512 places
 // that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 1575 us unsplit, 1162 us
-// and 19 us for the join in 2 chunks).  With a window a tile sees a window's worth, but the sinks' tiles every query: those
-// are taken apart, in up to 16 chunks (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: 1008 us
-// unsplit, 198 us and 5 us for the join in 16 chunks).
+// and 19 us for the join in 2 chunks).  Few tiles of long sequences (kQKeys): one workgroup for each place,
+// in chunks down to 384 rows (1024 tokens, 4 heads of 128: backward 71 us with whole tiles, 52 us).  With
+// a window a tile sees a window's worth, but the sinks' tiles every query: those are taken apart, in
+// chunks half as long as the others' (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: dk / dv 1008 us
+// unsplit, 198 us and 5 us for the join in 14 chunks; 4096 tokens, 16 / 1 heads of 64, window 512, 4 sinks:
+// backward 172 us in 16 chunks, 87 us in 64).
 AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks) {
   constexpr long long kBwdTarget = 1024, kBwdPartBytes = 512ll << 20;
   AttnBwdPlan p{};
   const long long slots = attn_slots(Tkv, n_seq, kAttnK), units = slots * n_kv_heads, group = n_heads / n_kv_heads;
   const long long rows = attn_step(head_dim), steps = ((long long)Tq + rows - 1) / rows * group;
   const long long bytes = (long long)(attn_part_floats(head_dim) * sizeof(float));
-  const long long min_steps = attn_min_steps(head_dim);
+  const bool few = units > 0 && units < kQTarget / 2 && Tq >= kQKeys * n_seq;
+  const long long min_steps = (few ? 384 : 1024) / rows;
+  p.sink_min = (int)(1024 / rows);
+  p.min_steps = (int)min_steps;
   const bool windowed = window > 0 && window < Tq;
   p.most = (int)std::min(steps, windowed ? ((long long)window + kAttnK + 2 * rows - 2) / rows * group : steps);
   p.splits = p.sink_splits = 1;
   if (units > 0) {
-    const long long target = windowed ? kBwdTarget / 2 : kBwdTarget;  // a window's tiles are equally long
+    const long long target = windowed || few ? kBwdTarget / 2 : kBwdTarget;  // a window's tiles are equally long
     p.splits = (int)std::max(1ll, std::min({(target + units - 1) / units, 16ll,
                                             ((long long)p.most + min_steps - 1) / min_steps,
                                             kBwdPartBytes / (units * bytes)}));
     if (windowed && sinks > 0) {
       const long long per_seq = (std::min((long long)sinks, (long long)Tkv) + kAttnK - 1) / kAttnK;
       const long long tiles = per_seq * n_seq;
+      const long long per = std::max((long long)p.sink_min, ((long long)p.most / p.splits + 1) / 2);
       const long long n = tiles <= 0 ? 1
-                                     : std::min({2 * kBwdTarget / (tiles * n_kv_heads), 16ll,
-                                                 (steps + min_steps - 1) / min_steps,
+                                     : std::min({2 * kBwdTarget / (tiles * n_kv_heads), 64ll, (steps + per - 1) / per,
                                                  kBwdPartBytes / (tiles * n_kv_heads * bytes)});
       if (n > 1) {
         p.sink_splits = (int)n;

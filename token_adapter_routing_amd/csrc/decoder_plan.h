@@ -31,10 +31,11 @@ size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, 
 // Query rows per step of the dk / dv pass: with heads of 64 twice as many fit in LDS beside three
 // waves per SIMD, which halves the waits between steps.
 MOLORA_HD constexpr int attn_step(int head_dim) { return head_dim == 64 ? 64 : 32; }
-MOLORA_HD constexpr int attn_min_steps(int head_dim) { return 1024 / attn_step(head_dim); }  // per chunk
 struct AttnBwdPlan {
   int splits, sink_splits, sink_tiles;
-  int most;  // steps of the longest tile that is not a sinks' tile
+  int most;       // steps of the longest tile that is not a sinks' tile
+  int min_steps;  // per chunk of it
+  int sink_min;   // per chunk of a sinks' tile
   int q_splits;
   size_t lse_off, delta_off, part_off, q_part_off, total;
 };
