@@ -484,3 +484,13 @@ def test_binding_refusals():
     with pytest.raises(m.MoloraError, match="head_dim"):
         x = torch.zeros(8, 2, 96, dtype=torch.bfloat16, device="cuda")
         m.molora_attn_forward(x, x, x, off)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,kv_lens,Hq,Hkv", [([2048], [2048], 16, 2), ([2304], [2500], 13, 1), ([1500, 3, 1300], [1500, 900, 1400], 3, 3)])
+def test_long_tiles_split_among_many(lens, kv_lens, Hq, Hkv, D):
+    """As many queries as keys: the long tiles are split into chunks of one length, short ones stay whole."""
+    m = need_gpu()
+    c = Case(lens, kv_lens, Hq, Hkv, D, seed=50)
+    assert m.molora_attn_forward_workspace(c.q.cuda(), c.k.cuda(), c.off()[0]) > 0
+    run(m, c)

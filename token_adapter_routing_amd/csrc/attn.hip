@@ -310,12 +310,14 @@ __device__ __forceinline__ Place place(const AttnArgs& a, int slots, unsigned id
   return {(int)(hk * g + rest % g), (int)hk, (int)(at - chunk * slots), (int)chunk};
 }
 
-// A query tile's key tiles split over up to `splits` workgroups, at least kAttnMinTiles each.
+// A query tile's key tiles split over up to `splits` workgroups, at least kAttnMinTiles each; without a
+// window by the sequence's longest tile, so that its chunks are equally long.
 struct Chunks {
   int per, n;
 };
-__device__ __forceinline__ Chunks key_chunks(int tiles, int splits) {
-  const int per = max((tiles + splits - 1) / splits, kAttnMinTiles);
+__device__ __forceinline__ Chunks key_chunks(const Mask& m, int tiles, int Lk, int splits) {
+  const int longest = m.window ? tiles : (Lk + kBN - 1) / kBN;
+  const int per = max((longest + splits - 1) / splits, kAttnMinTiles);
   return {per, max((tiles + per - 1) / per, 1)};
 }
 
@@ -347,7 +349,7 @@ __device__ __forceinline__ QTile q_tile(const AttnArgs& a, int slots, unsigned i
   x.q0 = t.a.lo, x.k0 = t.b.lo, x.Lk = t.b.n, x.last = t.a.n - 1, x.row0 = t.row0;
   x.m = Mask{x.Lk - t.a.n, a.window, a.sinks};
   x.kt = key_tiles(x.m, x.row0 + x.m.shift, min(x.row0 + kAttnQ - 1, x.last) + x.m.shift, x.Lk);
-  const Chunks ch = key_chunks(x.kt.n, splits);
+  const Chunks ch = key_chunks(x.m, x.kt.n, x.Lk, splits);
   x.chunks = ch.n;
   x.it0 = x.chunk * ch.per;
   x.it1 = min(x.it0 + ch.per, x.kt.n);
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(256) void attn_fwd_join_k(AttnArgs a, int slots) {
   const Mask m{t.b.n - t.a.n, a.window, a.sinks};
   const int last = t.a.n - 1;
   const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.b.n);
-  const Chunks ch = key_chunks(kt.n, a.splits);
+  const Chunks ch = key_chunks(m, kt.n, t.b.n, a.splits);
   const int row = 32 * quarter + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (D / 8);
   if (ch.n == 1 || t.row0 + row > last) return;
   const size_t next = (size_t)slots * a.Hq * attn_fwd_part_floats(D);
@@ -785,7 +787,7 @@ __global__ __launch_bounds__(256) void attn_dq_join_k(AttnBackwardArgs b, int sl
   const Mask m{t.b.n - t.a.n, a.window, a.sinks};
   const int last = t.a.n - 1;
   const KeyTiles kt = key_tiles(m, t.row0 + m.shift, min(t.row0 + kAttnQ - 1, last) + m.shift, t.b.n);
-  const Chunks ch = key_chunks(kt.n, b.q_splits);
+  const Chunks ch = key_chunks(m, kt.n, t.b.n, b.q_splits);
   const int row = 32 * quarter + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (D / 8);
   if (ch.n == 1 || t.row0 + row > last) return;
   const size_t next = (size_t)slots * a.Hq * kAttnQ * D;
