@@ -704,12 +704,15 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(Att
   const float lse2 = lse == -INFINITY ? 0.f : lse * kLog2e;  // a row that sees nothing: its scores are all -inf
   if (t.chunk == 0 && h == 0 && r0 + n <= last) {
     b.lse2[stat] = lse2;
-    b.delta[stat] = delta;
+    b.delta[stat] = -delta;
   }
   f32x16_t dq[D / 32];
 #pragma unroll
   for (int mb = 0; mb < D / 32; ++mb) dq[mb] = f32x16_t{};
   const float c = a.scale * kLog2e;
+  f32x16_t from;  // dP - delta is summed from here
+#pragma unroll
+  for (int i = 0; i < 16; ++i) from[i] = -delta;
   Fetch<D, kBN> fetch;
   fetch.init(lane, wave);
   const LaneOff lo = lane_off<D>(lane);
@@ -725,7 +728,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(Att
       const bool all = sees_all(m, p_lo, p_hi, j0, j0 + kBN - 1);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
-        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+        f32x16_t s = f32x16_t{}, dp = from;
 #pragma unroll
         for (int st = 0; st < D / 16; ++st) {
           s = mfma32x32x16(row_frag<D>(K, lo, 32 * blk, st), q[st], s);
@@ -734,7 +737,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(Att
         reads_ahead<D / 16, 2, 2, 3>();
         if (!all) hide(s, m, p, j0 + 32 * blk, h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+        for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], c, -lse2)) * dp[i];
         const bf16x8_t df[2] = {acc_frag(s, 0), acc_frag(s, 1)};
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -932,7 +935,7 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
         float w = 0.f, ds = 0.f;
         if (see) {
           w = exp2_hw(fmaf(dot_rows<D>(s.q + lane * a.q.token, kp), c, -s.lse2[lane]));
-          ds = w * (dot_rows<D>(s.g + lane * b.dout.token, vp) - s.delta[lane]);
+          ds = w * (dot_rows<D>(s.g + lane * b.dout.token, vp) + s.delta[lane]);
         }
         const uint64_t who = __ballot(see);
         xv.add(who, w, s.g, b.dout.token, lane);
@@ -963,8 +966,11 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kBQ = attn_step(D), kTileB = kBQ * Tile<D>::kRow;
+  // dP - delta is summed from -delta where vector instructions bound the pass (8192 tokens, 32 / 8 heads of
+  // 64, window 1024: 186 -> 182 us; with 128 values the sums' start would wait for it: 1171 -> 1187 us).
+  constexpr bool kFrom = D == 64;
   __shared__ __attribute__((aligned(16))) char ldsQ0[kTileB], ldsQ1[kTileB], ldsG0[kTileB], ldsG1[kTileB];
-  __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, row sums
+  __shared__ __attribute__((aligned(16))) float st0[2 * kBQ], st1[2 * kBQ];  // lse in base 2, -row sums
   // The workgroup's V stays in LDS: beside K's operands and the sums of dK and dV in registers it would
   // cost a wave per SIMD (4 x 4096 tokens, 16 heads, when it was moved: 64 values 451 us with V in
   // registers and two waves, 402 us with three; 128 values 1438 us with one wave, 794 us with two).
@@ -1028,6 +1034,14 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
     if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
       const bool all = i0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
       f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+      if constexpr (kFrom) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dp[4 * g + i] = d4[i];
+        }
+      }
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
         s = mfma32x32x16(row_frag<D>(Q, lo, sb, st), kf[st], s);
@@ -1044,12 +1058,13 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + sb + 8 * g + 4 * h);
-        const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
+        f32x4_t d4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (!kFrom) d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float pv = exp2_hw(fmaf(s[4 * g + i], c, -l4[i]));
           s[4 * g + i] = pv;
-          dp[4 * g + i] = pv * (dp[4 * g + i] - d4[i]);
+          dp[4 * g + i] = pv * (kFrom ? dp[4 * g + i] : dp[4 * g + i] + d4[i]);
         }
       }
       const bf16x8_t pf[2] = {acc_frag(s, 0), acc_frag(s, 1)}, df[2] = {acc_frag(dp, 0), acc_frag(dp, 1)};

@@ -44,7 +44,7 @@ struct AttnBackwardArgs {
   AttnArgs f;  // o and lse as the forward wrote them
   Rows dout, dq, dk, dv;
   float* lse2;   // workspace [Hq][Tq]: lse in base 2
-  float* delta;  // workspace [Hq][Tq]: rowsum(dO O)
+  float* delta;  // workspace [Hq][Tq]: -rowsum(dO O)
   int q_splits;   // attn_q_splits
   float* q_part;  // workspace: the split query tiles' sums
   int splits, sink_splits, sink_tiles, most, min_steps, sink_min;  // attn_bwd_plan
