@@ -430,12 +430,11 @@ __device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t
 // queries by 128 values are the 223 registers that leave two waves per SIMD; 64 keys because two
 // workgroups' double buffers of K and V (64 KiB each) then fit a CU.
 //
-// Bound by the issue of matrix and vector instructions together (per 64 keys a wave has 32 products of
-// 32 cycles at two waves per SIMD, and about 190 vector instructions of softmax between them) and by
-// the clock they leave (about 1.8 GHz): 8192 tokens, 32 / 8 heads of 128, 533 us = 1031 TFLOP/s, the
-// matrix units busy 54 % of the cycles, no bank conflicts; without copies and barriers the rest takes
-// 479 us.  Heads of 64 do half the products per softmax: 4 x 4096 tokens, 16 heads 179 us = 768 TFLOP/s.
-// Short calls: one tile 8.6 us, each further 64 keys about 1.07 us.
+// Bound by the matrix units at the clock they leave (54 % busy at 1.8 GHz; the library's product of 8192^3
+// goes to 71 % at 1.5): 8192 tokens, 32 / 8 heads of 128, 540 us = 1018 TFLOP/s, no bank conflicts; without
+// copies and barriers the rest takes 479 us.  Heads of 64 do half the products per softmax, whose vector
+// instructions then bound them: 4 x 4096 tokens, 16 heads 166 us = 826 TFLOP/s.  Short calls: one tile
+// 8.6 us, each further 64 keys about 1.07 us.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
@@ -660,8 +659,8 @@ __device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, u
 // the keys as the forward does.  A kernel of its own, so that dQ is summed in registers in one order:
 // together with dK and dV it would need atomics or a pass over partial sums.  The price is S and dP
 // twice, seven products for five.
-// Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 740 us = 1113 TFLOP/s, the matrix units busy
-// 60 % of the cycles (three products for one exponential); heads of 64, window 1024: 128 us.
+// Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 745 us = 1107 TFLOP/s, the matrix units busy
+// 61 % of the cycles (three products for one exponential); heads of 64, window 1024: 122 us.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
@@ -962,7 +961,7 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
 // Bound as the forward, and by the waits between steps: 8192 tokens, 32 / 8 heads of 128, 1150 us = 956
 // TFLOP/s, the matrix units busy 48 % of the cycles, waves waiting for copies and each other 28 %
 // (with 128 values a step holds 32 rows: Q, dO and V fill the LDS of two workgroups); heads of 64,
-// 64 rows per step, 4 x 4096 tokens, 16 heads 318 us = 866 TFLOP/s.
+// 64 rows per step, 4 x 4096 tokens, 16 heads 295 us = 931 TFLOP/s.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kBQ = attn_step(D), kTileB = kBQ * Tile<D>::kRow;
