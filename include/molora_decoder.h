@@ -90,6 +90,7 @@ int molora_route_scores_backward(const float *logits, const int32_t *idx, const 
  *   q_off, kv_off  device int32 [n_seq + 1], non-decreasing, kv_off NULL: the
  *           same as q_off.  Offsets are limited to [0, Tq] and [0, Tkv].
  *   window  0: none (sinks has no effect); else at least 1
+ * o must not overlap q, k or v (parts of one buffer may interleave).
  * Rows of o and entries of lse outside every sequence are left as they were,
  * and rows of q, k and v outside every sequence are not read into any result.
  * Infinities and NaN reach the results of the pairs that see them and no

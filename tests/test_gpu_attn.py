@@ -494,3 +494,13 @@ def test_long_tiles_split_among_many(lens, kv_lens, Hq, Hkv, D):
     c = Case(lens, kv_lens, Hq, Hkv, D, seed=50)
     assert m.molora_attn_forward_workspace(c.q.cuda(), c.k.cuda(), c.off()[0]) > 0
     run(m, c)
+
+
+def test_many_sequences_with_split_keys():
+    """More sequences than a wave has lanes, each with few queries before many keys."""
+    m = need_gpu()
+    lens = [1 + i % 3 for i in range(70)]
+    kv = [700 + (i * 37) % 300 for i in range(70)]
+    c = Case(lens, kv, 2, 1, 64, seed=51)
+    assert m.molora_attn_forward_workspace(c.q.cuda(), c.k.cuda(), c.off()[0]) > 0
+    run(m, c)

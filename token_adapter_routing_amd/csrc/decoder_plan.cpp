@@ -28,12 +28,12 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
 // with as many queries as keys it is half of the longest one, which then sets the time (8192 tokens, 4 heads
 // of 128, 260 tiles: forward 155 us whole, 108 us split; 4096 tokens, 8 heads, 264 tiles: 79 and 62 us).
 // Sequences of kQKeys keys on average (512 keys gain nothing: 15.8 us whole, 17.1 us split; 1024 keys
-// 24.4 us whole, 18.4 us split), and of more with more tiles, whose parts have to be written and
-// joined too (2048 tokens, 16 heads, 272 tiles: 43 and 41 us; 1024 tokens, 32 heads, 288 tiles: 26 and 34 us).
+// 24.4 us whole, 18.4 us split); of more where the tiles alone give every CU a workgroup, whose parts have
+// to be written and joined too (2048 tokens, 16 heads, 272 tiles: 43 and 41 us; 1024 tokens, 32 heads, 288 tiles: 26 and 34 us).
 constexpr long long kQTarget = 512, kQKeys = 768;
 int attn_q_splits(int Tq, int Tkv, int n_seq, int n_heads, int window, int sinks) {
   const long long units = attn_slots(Tq, n_seq, kAttnQ) * n_heads;
-  if (units <= 0 || Tkv == 0 || Tkv < n_seq * std::max(kQKeys, 7 * units)) return 1;
+  if (units <= 0 || Tkv == 0 || Tkv < n_seq * (units < kQTarget / 2 ? kQKeys : 7 * units)) return 1;
   long long keys = Tkv, target = kQTarget;
   if (window > 0 && window < Tkv) keys = std::min(keys, (long long)window + sinks + 2 * kAttnQ);
   else target = kQTarget * 2 * Tkv / (2ll * Tkv - std::min(Tq, Tkv));
