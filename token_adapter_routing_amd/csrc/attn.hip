@@ -617,8 +617,8 @@ namespace {
 
 // attn_dq_k's rows that are taken again (see fwd_again).
 template <int D>
-__device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, uint32_t again, int wave, int lane, float lse2,
-                                         float delta) {
+__device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, uint32_t again, int wave, int lane,
+                                         float lse2, float delta) {
   const AttnArgs& a = b.f;
   const QTile t = q_tile(a, slots, group_again(), b.q_splits);
   const uint16_t* kb = a.k.p + (long long)t.k0 * a.k.token + t.hk * a.k.head;
@@ -1028,66 +1028,66 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
     asm volatile("" : "+v"(lo.row), "+v"(lo.col));
 #pragma unroll
     for (int sb = kBQ - 32; sb >= 0; sb -= 32) {
-    const int i0 = s0 + sb;
-    const int p_lo = i0 + m.shift, p_hi = min(i0 + 31, Lq - 1) + m.shift;
-    if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
-      const bool all = i0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
-      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
-      if constexpr (kFrom) {
+      const int i0 = s0 + sb;
+      const int p_lo = i0 + m.shift, p_hi = min(i0 + 31, Lq - 1) + m.shift;
+      if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
+        const bool all = i0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
+        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+        if constexpr (kFrom) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dp[4 * g + i] = d4[i];
+          }
+        }
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {
+          s = mfma32x32x16(row_frag<D>(Q, lo, sb, st), kf[st], s);
+          dp = mfma32x32x16(row_frag<D>(G, lo, sb, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
+        }
+        reads_ahead<D / 16, 2, 3, 3>();
+        if (!all) {
+          // the queries that see key j: a range of rows, here relative to the lane's first
+          const int first = j - m.shift - i0 - 4 * h, rows = Lq - i0 - 4 * h;
+          const int end = m.window == 0 || j < m.sinks ? rows : min(first + m.window, rows);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = acc_row(i, 0) >= first && acc_row(i, 0) < end ? s[i] : -INFINITY;
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
+          const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + sb + 8 * g + 4 * h);
+          f32x4_t d4{0.f, 0.f, 0.f, 0.f};
+          if constexpr (!kFrom) d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dp[4 * g + i] = d4[i];
+          for (int i = 0; i < 4; ++i) {
+            const float pv = exp2_hw(fmaf(s[4 * g + i], c, -l4[i]));
+            s[4 * g + i] = pv;
+            dp[4 * g + i] = pv * (kFrom ? dp[4 * g + i] : dp[4 * g + i] + d4[i]);
+          }
         }
-      }
+        const bf16x8_t pf[2] = {acc_frag(s, 0), acc_frag(s, 1)}, df[2] = {acc_frag(dp, 0), acc_frag(dp, 1)};
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int st = 0; st < D / 16; ++st) {
-        s = mfma32x32x16(row_frag<D>(Q, lo, sb, st), kf[st], s);
-        dp = mfma32x32x16(row_frag<D>(G, lo, sb, st), row_frag<D>(ldsV, lo, 32 * wave, st), dp);
-      }
-      reads_ahead<D / 16, 2, 3, 3>();
-      if (!all) {
-        // the queries that see key j: a range of rows, here relative to the lane's first
-        const int first = j - m.shift - i0 - 4 * h, rows = Lq - i0 - 4 * h;
-        const int end = m.window == 0 || j < m.sinks ? rows : min(first + m.window, rows);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = acc_row(i, 0) >= first && acc_row(i, 0) < end ? s[i] : -INFINITY;
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(ls + sb + 8 * g + 4 * h);
-        f32x4_t d4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (!kFrom) d4 = *reinterpret_cast<const f32x4_t*>(ls + kBQ + sb + 8 * g + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float pv = exp2_hw(fmaf(s[4 * g + i], c, -l4[i]));
-          s[4 * g + i] = pv;
-          dp[4 * g + i] = pv * (kFrom ? dp[4 * g + i] : dp[4 * g + i] + d4[i]);
-        }
-      }
-      const bf16x8_t pf[2] = {acc_frag(s, 0), acc_frag(s, 1)}, df[2] = {acc_frag(dp, 0), acc_frag(dp, 1)};
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int mb = 0; mb < D / 32; ++mb) {
-          dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pf[st], dv[mb]);
-          dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), df[st], dk[mb]);
-        }
-      reads_ahead<D / 8, 1, 2, 4>();
-      if constexpr (FINE) {
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const bf16x8_t pr = acc_rest(s, st, pf[st]), dr = acc_rest(dp, st, df[st]);
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int mb = 0; mb < D / 32; ++mb) {
-            dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pr, dv[mb]);
-            dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), dr, dk[mb]);
+            dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pf[st], dv[mb]);
+            dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), df[st], dk[mb]);
+          }
+        reads_ahead<D / 8, 1, 2, 4>();
+        if constexpr (FINE) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const bf16x8_t pr = acc_rest(s, st, pf[st]), dr = acc_rest(dp, st, df[st]);
+#pragma unroll
+            for (int mb = 0; mb < D / 32; ++mb) {
+              dv[mb] = mfma32x32x16(col_frag<D>(G, lo, sb + 16 * st, mb), pr, dv[mb]);
+              dk[mb] = mfma32x32x16(col_frag<D>(Q, lo, sb + 16 * st, mb), dr, dk[mb]);
+            }
           }
         }
       }
-    }
     }
     tiles_ready();
   };
@@ -1168,8 +1168,8 @@ hipError_t backward(const AttnBackwardArgs& b, hipStream_t s) {
     }
   }
   const long long sinks = (long long)b.sink_tiles * a.n_seq;
-  hipLaunchKernelGGL((attn_dkv_k<D, FINE>), dim3((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv)), dim3(256), 0, s, b,
-                     (int)ks);
+  const dim3 grid((unsigned)((sinks * b.sink_splits + ks * b.splits) * a.Hkv));
+  hipLaunchKernelGGL((attn_dkv_k<D, FINE>), grid, dim3(256), 0, s, b, (int)ks);
   const hipError_t e = hipGetLastError();
   const long long joins = sinks + (b.splits > 1 ? ks : 0);
   if (e != hipSuccess || joins == 0) return e;

@@ -29,7 +29,8 @@ DecodePlan decode_plan(int n_seq, int n_heads, int n_kv_heads, int head_dim, int
 // of 128, 260 tiles: forward 155 us whole, 108 us split; 4096 tokens, 8 heads, 264 tiles: 79 and 62 us).
 // Sequences of kQKeys keys on average (512 keys gain nothing: 15.8 us whole, 17.1 us split; 1024 keys
 // 24.4 us whole, 18.4 us split); of more where the tiles alone give every CU a workgroup, whose parts have
-// to be written and joined too (2048 tokens, 16 heads, 272 tiles: 43 and 41 us; 1024 tokens, 32 heads, 288 tiles: 26 and 34 us).
+// to be written and joined too (2048 tokens, 16 heads, 272 tiles: 43 and 41 us; 1024 tokens, 32 heads, 288
+// tiles: 26 and 34 us).
 constexpr long long kQTarget = 512, kQKeys = 768;
 int attn_q_splits(int Tq, int Tkv, int n_seq, int n_heads, int window, int sinks) {
   const long long units = attn_slots(Tq, n_seq, kAttnQ) * n_heads;
@@ -51,11 +52,11 @@ size_t attn_fwd_ws_bytes(int Tq, int Tkv, int n_seq, int n_heads, int head_dim, 
 // one sets the time: chunks until there are kBwdTarget workgroups, two for each of the 512 places
 // that two waves per SIMD leave (8192 tokens, 32 / 8 heads of 128: dk / dv 1575 us unsplit, 1162 us
 // and 19 us for the join in 2 chunks).  Few tiles of long sequences (kQKeys): one workgroup for each place,
-// in chunks down to 384 rows (1024 tokens, 4 heads of 128: backward 71 us with whole tiles, 52 us).  With
-// a window a tile sees a window's worth, but the sinks' tiles every query: those are taken apart, in
-// chunks half as long as the others' (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: dk / dv 1008 us
-// unsplit, 198 us and 5 us for the join in 14 chunks; 4096 tokens, 16 / 1 heads of 64, window 512, 4 sinks:
-// backward 172 us in 16 chunks, 87 us in 64).
+// in chunks down to 384 rows (1024 tokens, 4 heads of 128: backward 71 us with whole tiles, 52 us).
+// With a window a tile sees a window's worth, but the sinks' tiles every query: those are taken apart, in
+// chunks half as long as the others' (8192 tokens, 32 / 8 heads of 64, window 1024, 16 sinks: dk / dv
+// 1008 us unsplit, 198 us and 5 us for the join in 14 chunks; 4096 tokens, 16 / 1 heads of 64, window 512,
+// 4 sinks: backward 172 us in 16 chunks, 87 us in 64).
 AttnBwdPlan attn_bwd_plan(int Tq, int Tkv, int n_seq, int n_heads, int n_kv_heads, int head_dim, int window, int sinks) {
   constexpr long long kBwdTarget = 1024, kBwdPartBytes = 512ll << 20;
   AttnBwdPlan p{};
