@@ -1008,8 +1008,14 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   const uint16_t* gb = b.dout.p + (long long)qr.lo * b.dout.token;
   // The queries from the last on: every key tile of a causal sequence ends there, so the workgroups
   // that run together read the same rows.
-  auto request = [&](int it, char* __restrict__ Q, char* __restrict__ G, float* __restrict__ st) {
-    const int hq = hk * group + it / nt, i0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
+  int head = it0 < it1 ? it0 / nt : 0, back = it0 - head * nt, i0 = 0;  // of the next request; rows requested last
+  auto request = [&](char* __restrict__ Q, char* __restrict__ G, float* __restrict__ st) {
+    const int hq = hk * group + head;
+    i0 = (t.t_lo + nt - 1 - back) * kBQ;
+    if (++back == nt) {
+      back = 0;
+      ++head;
+    }
     fetch(Q, qb + hq * a.q.head, qs, i0, Lq - 1, wave);
     fetch(G, gb + hq * b.dout.head, gs, i0, Lq - 1, wave);
     if (wave < 2 * kBQ / kWave) {
@@ -1021,17 +1027,17 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
   };
   auto step = [&](int it, const char* __restrict__ Q, const char* __restrict__ G, const float* __restrict__ ls,
                   char* __restrict__ nextQ, char* __restrict__ nextG, float* __restrict__ next_st) {
-    if (it + 1 < it1) request(it + 1, nextQ, nextG, next_st);
-    const int s0 = (t.t_lo + nt - 1 - it % nt) * kBQ;
+    const int s0 = i0;
+    if (it + 1 < it1) request(nextQ, nextG, next_st);
     LaneOff lo = lo0;
     // opaque: the operands' addresses are made when needed; kept in registers they would spill others
     asm volatile("" : "+v"(lo.row), "+v"(lo.col));
 #pragma unroll
     for (int sb = kBQ - 32; sb >= 0; sb -= 32) {
-      const int i0 = s0 + sb;
-      const int p_lo = i0 + m.shift, p_hi = min(i0 + 31, Lq - 1) + m.shift;
+      const int r0 = s0 + sb;
+      const int p_lo = r0 + m.shift, p_hi = min(r0 + 31, Lq - 1) + m.shift;
       if (jw < Lk && !sees_none(m, p_lo, p_hi, jw, jw + 31)) {
-        const bool all = i0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
+        const bool all = r0 + 32 <= Lq && sees_all(m, p_lo, p_hi, jw, jw + 31);
         f32x16_t s = f32x16_t{}, dp = f32x16_t{};
         if constexpr (kFrom) {
 #pragma unroll
@@ -1049,7 +1055,7 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
         reads_ahead<D / 16, 2, 3, 3>();
         if (!all) {
           // the queries that see key j: a range of rows, here relative to the lane's first
-          const int first = j - m.shift - i0 - 4 * h, rows = Lq - i0 - 4 * h;
+          const int first = j - m.shift - r0 - 4 * h, rows = Lq - r0 - 4 * h;
           const int end = m.window == 0 || j < m.sinks ? rows : min(first + m.window, rows);
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = acc_row(i, 0) >= first && acc_row(i, 0) < end ? s[i] : -INFINITY;
@@ -1091,7 +1097,7 @@ __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(At
     }
     tiles_ready();
   };
-  if (it0 < it1) request(it0, ldsQ0, ldsG0, st0);
+  if (it0 < it1) request(ldsQ0, ldsG0, st0);
   tiles_ready();
   for (int it = it0; it < it1; it += 2) {
     step(it, ldsQ0, ldsG0, st0, ldsQ1, ldsG1, st1);
