@@ -431,7 +431,7 @@ __device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t
 // workgroups' double buffers of K and V (64 KiB each) then fit a CU.
 //
 // Bound by the matrix units at the clock they leave (54 % busy at 1.8 GHz; the library's product of 8192^3
-// goes to 71 % at 1.5): 8192 tokens, 32 / 8 heads of 128, 540 us = 1018 TFLOP/s, no bank conflicts; without
+// goes to 71 % at 1.5): 8192 tokens, 32 / 8 heads of 128, 532 us = 1033 TFLOP/s, no bank conflicts; without
 // copies and barriers the rest takes 479 us.  Heads of 64 do half the products per softmax, whose vector
 // instructions then bound them: 4 x 4096 tokens, 16 heads 166 us = 826 TFLOP/s.  Short calls: one tile
 // 8.6 us, each further 64 keys about 1.07 us.
@@ -659,7 +659,7 @@ __device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, u
 // the keys as the forward does.  A kernel of its own, so that dQ is summed in registers in one order:
 // together with dK and dV it would need atomics or a pass over partial sums.  The price is S and dP
 // twice, seven products for five.
-// Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 745 us = 1107 TFLOP/s, the matrix units busy
+// Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 730 us = 1129 TFLOP/s, the matrix units busy
 // 61 % of the cycles (three products for one exponential); heads of 64, window 1024: 122 us.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
@@ -958,10 +958,10 @@ __device__ __forceinline__ void dkv_again(const AttnBackwardArgs& b, int slots, 
 // of every query head that reads it (or one chunk of them, whose sums go to the workspace).  S and
 // dP are computed with the queries down, so that P and dS are the right operands of dV^T = dO^T P
 // and dK^T = Q^T dS.
-// Bound as the forward, and by the waits between steps: 8192 tokens, 32 / 8 heads of 128, 1150 us = 956
-// TFLOP/s, the matrix units busy 48 % of the cycles, waves waiting for copies and each other 28 %
+// Bound as the forward, and by the waits between steps: 8192 tokens, 32 / 8 heads of 128, 1115 us = 986
+// TFLOP/s, the matrix units busy 50 % of the cycles, waves waiting for copies and each other 28 %
 // (with 128 values a step holds 32 rows: Q, dO and V fill the LDS of two workgroups); heads of 64,
-// 64 rows per step, 4 x 4096 tokens, 16 heads 295 us = 931 TFLOP/s.
+// 64 rows per step, 4 x 4096 tokens, 16 heads 287 us = 957 TFLOP/s.
 template <int D, bool FINE>
 __global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dkv_k(AttnBackwardArgs b, int slots) {
   constexpr int kBQ = attn_step(D), kTileB = kBQ * Tile<D>::kRow;
