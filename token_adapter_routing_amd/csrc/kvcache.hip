@@ -10,8 +10,10 @@ namespace molora {
 // ------------------------------------------------------------------------------- append
 // A wave per token: the token's sequence by a search in q_off, its page and row, then its
 // 2 Hkv rows of D values, D / 8 lanes per row (16-byte pieces), 64 / (D / 8) rows at a time.
-// Memory-bound: every row is read once and written once (15361 tokens, 8 heads of 128, bf16: 126 MB in
-// 21.6 us, 5.8 TB/s; 256 single tokens in 8 bits 5.4 us, which is the launch and three dependent loads).
+// Memory-bound: every row is read once and written once, past the caches, which nothing that follows soon
+// reads it from (15 prompts, 8 heads of 128, bf16, 126 MB of rows not in any cache: 27.5 us with ordinary
+// stores, 21.8 us = 6.1 TB/s; 16384 tokens in 8 bits 25.4 and 24.4 us).  Several rows requested at once per
+// lane gain nothing (28.4 us).  256 single tokens in 8 bits 5.5 us: the launch and three dependent loads.
 //
 // e4m3: the row's factor is the smallest power of two that brings its largest finite magnitude
 // within 448 (a floating format keeps its relative precision under any factor, and a power of two
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(256) void kv_append_k(KvAppendArgs a) {
     const u32x4_t x = ld16(src.p + t * src.token + head * src.head + 8 * piece);
     const long long row = row0 + (long long)head * page_size;
     if constexpr (!E4M3) {
-      st16(reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + row * D + 8 * piece, x);
+      st16_nt(reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + row * D + 8 * piece, x);
     } else {
       float f[8], big = 0.f;
 #pragma unroll
@@ -72,8 +74,9 @@ __global__ __launch_bounds__(256) void kv_append_k(KvAppendArgs a) {
       lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
       int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
       hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + row * D + 8 * piece) =
-          make_uint2(lo, hi);
+      __builtin_nontemporal_store(
+          (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo,
+          reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + row * D + 8 * piece));
       if (piece == 0) (is_v ? a.c.v_scale : a.c.k_scale)[row] = (uint8_t)(n + 127);
     }
   }
