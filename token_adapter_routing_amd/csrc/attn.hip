@@ -449,7 +449,7 @@ __device__ __forceinline__ void fwd_again(const AttnArgs& a, int slots, uint32_t
 // goes to 71 % at 1.5): 8192 tokens, 32 / 8 heads of 128, 532 us = 1033 TFLOP/s, no bank conflicts; without
 // copies and barriers the rest takes 479 us.  Heads of 64 do half the products per softmax, whose vector
 // instructions then bound them: 4 x 4096 tokens, 16 heads 166 us = 826 TFLOP/s.  Short calls: one tile
-// 8.6 us, each further 64 keys about 1.07 us.
+// 8.2 us, each further 64 keys about 1.07 us.
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_fwd_k(AttnArgs a, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
@@ -678,7 +678,7 @@ __device__ __forceinline__ void dq_again(const AttnBackwardArgs& b, int slots, u
 // Bound as the forward: 8192 tokens, 32 / 8 heads of 128, 730 us = 1129 TFLOP/s, the matrix units busy
 // 61 % of the cycles (three products for one exponential); heads of 64, window 1024: 122 us.
 template <int D, bool FINE>
-__global__ __launch_bounds__(256, D == 64 ? 3 : FINE ? 1 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
+__global__ __launch_bounds__(256, FINE ? 1 : D == 64 ? 3 : 2) void attn_dq_k(AttnBackwardArgs b, int slots) {
   constexpr int kTileB = kBN * Tile<D>::kRow;
   __shared__ __attribute__((aligned(16))) char ldsK0[kTileB], ldsK1[kTileB], ldsV0[kTileB], ldsV1[kTileB];
   const AttnArgs& a = b.f;
